@@ -1,0 +1,200 @@
+/*
+ * qbl cache: the serving operators around the dual-path linear on AMD Instinct
+ * MI355X (gfx950): a paged key/value cache held in 4 bits, attention over it
+ * (full, or through a sliding window with sinks) and the verification of
+ * drafted tokens.
+ *
+ * Conventions are those of qbl.h: every call returns a qbl_status, checks its
+ * host-visible arguments before it enqueues anything (on error nothing
+ * changed, qbl_last_error() describes it), only enqueues on `stream` without
+ * synchronising, allocates nothing, and lets no C++ exception out.  Every call
+ * may be captured into a HIP graph.  Calls that touch one cache are ordered by
+ * the stream they are enqueued on; callers order streams themselves.
+ *
+ * Whatever decides lengths, pages and slots lives in device memory, so a
+ * decode loop (extend, append, attend, verify, truncate) needs no host round
+ * trip.  Device-side arguments are checked by the kernels: an index outside
+ * its range is never followed (each call says what happens instead).
+ */
+#ifndef QBL_CACHE_H
+#define QBL_CACHE_H
+
+#include "qbl.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of activations. */
+#define QBL_T_F32 0
+#define QBL_T_F16 1
+#define QBL_T_BF16 2
+
+/* Limits. */
+#define QBL_KV_MAX_ENTRIES 1024 /* entries of one extend, fork or truncate call */
+#define QBL_KV_MAX_TOKENS (1 << 24) /* max_pages * page_tokens of a cache */
+#define QBL_KV_MAX_DRAFT 256    /* drafted tokens per request of qbl_verify */
+
+/* A cache: caller-owned device memory and its shape.
+ *
+ * store  n_layers x n_pages pages of qbl_kv_page_bytes bytes, 16-byte aligned.
+ *        A page holds page_tokens tokens (32, 64, 128 or 256) of every
+ *        key/value head: [kv head][page_tokens/32 tiles][tile bytes].  A tile
+ *        is 32 tokens of one head, D = head_dim (64, 128 or 256) channels in
+ *        nb = D/32 blocks; each block of 32 channels of one token is a q4_sm
+ *        block of qbl.h (fp16 step d, fp16 minimum m, 4-bit codes, value
+ *        d*code + m: 5 bits per value).  Tile bytes, 32 D + 256 nb:
+ *          K codes  [max(1, D/128)][32 tokens][4 quads][min(nb, 4) blocks]
+ *                   32-bit words; a word holds channels 32 block + 8 quad +
+ *                   0..7, byte i = channel i low nibble, channel i + 4 high;
+ *          K scales [32 tokens][nb] 32-bit words d | m << 16;
+ *          V codes  [D/64][16 lanes][4 quads][4] words; word (c, lane, quad, n)
+ *                   holds channel 64 c + 16 n + lane, byte j = token
+ *                   4 quad + j low nibble, token 16 + 4 quad + j high;
+ *          V scales d, then m, each fp16 [nb][4 quads][8]: tokens 4 quad +
+ *                   0..3, then 16 + 4 quad + 0..3.
+ *        (The order is the operand order of the matrix instructions, so the
+ *        attention kernels load codes straight into registers.)
+ * refs   int32 per page: how many slots' tables hold it; 0 = free.
+ * lens   int32 per slot: tokens held.
+ * table  int32 n_slots x max_pages: page of a slot's tokens
+ *        [p*page_tokens, (p+1)*page_tokens); -1 where there is none.
+ * status int32: 0, or the status of the first page call that could not be
+ *        done (QBL_E_ARG a slot out of range, QBL_E_DUPLICATE a slot listed
+ *        twice, QBL_E_NOMEM too few free pages, QBL_E_LIMIT beyond max_pages,
+ *        QBL_E_STATE a fork into a slot in use or a missing page).  Such a
+ *        call changes nothing else.  It stays until the caller clears it.
+ * An empty cache has refs, lens and status 0 and the table -1; the store needs
+ * no initialisation. */
+typedef struct {
+  int32_t n_layers, n_pages, page_tokens, n_kv_heads, head_dim, n_slots, max_pages;
+  int32_t reserved; /* must be 0 */
+  void* store;
+  int32_t* refs;
+  int32_t* lens;
+  int32_t* table;
+  int32_t* status;
+} qbl_kv;
+
+/* Bytes of one page of one layer; 0 for unsupported sizes. */
+int64_t qbl_kv_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim);
+
+/* ---------------------------------------------------------------- pages ---
+ * slots, src, dst, counts and new_lens are device int32 arrays of n entries
+ * (1 <= n <= QBL_KV_MAX_ENTRIES); slots NULL means 0..n-1.  Free pages are
+ * always taken lowest index first, entry by entry, so results do not depend on
+ * scheduling. */
+
+/* Workspace of qbl_kv_extend and qbl_kv_compact (16-byte aligned, contents
+ * irrelevant) for calls of up to n entries. */
+qbl_status qbl_kv_pages_ws_bytes(const qbl_kv* kv, int32_t n, int64_t* bytes_out);
+
+/* Make room for counts[i] more tokens (negative: 0) in each slot and add them
+ * to lens.  A partly filled last page that other slots share is first copied,
+ * in all layers, to a page of the slot's own (of several entries sharing it,
+ * the last keeps it if nobody else holds it).  The new tokens' contents are
+ * written by qbl_kv_append.  All or nothing: see status. */
+qbl_status qbl_kv_extend(const qbl_kv* kv, const int32_t* slots, const int32_t* counts, int32_t n,
+                         void* ws, int64_t ws_bytes, void* stream);
+
+/* Give slot dst[i] (empty: length 0) the first prefix[i] tokens of slot src[i]
+ * (prefix NULL, or more than it holds: all of them) by sharing its pages; no
+ * cache contents move.  Sources are read as they were before the call. */
+qbl_status qbl_kv_fork(const qbl_kv* kv, const int32_t* src, const int32_t* dst, const int32_t* prefix,
+                       int32_t n, void* stream);
+
+/* Shorten each slot to new_lens[i] tokens (0 or less frees it; a length the
+ * slot does not have changes nothing) and drop the pages past it; a page whose
+ * last user drops it is free. */
+qbl_status qbl_kv_truncate(const qbl_kv* kv, const int32_t* slots, const int32_t* new_lens, int32_t n,
+                           void* stream);
+
+/* Move the used pages together: afterwards exactly the pages [0, used) are in
+ * use.  The k-th used page at or past index `used` moves, in all layers, to
+ * the k-th free page before it; tables and refs follow. */
+qbl_status qbl_kv_compact(const qbl_kv* kv, void* ws, int64_t ws_bytes, void* stream);
+
+/* Copy pages src[i] to dst[i] in all layers (any n >= 1; a pair with an index
+ * outside the cache is skipped).  No destination may be another pair's source
+ * or destination. */
+qbl_status qbl_kv_copy(const qbl_kv* kv, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/* ------------------------------------------------------- cache contents ---
+ * A call covers n entries of up to q_len new tokens each.  slots (device, NULL:
+ * 0..n-1) names each entry's slot, counts (device, NULL: q_len each; clamped to
+ * 0..q_len) its new tokens c, which are the slot's last: token j sits at
+ * position lens[slot] - c + j.  An entry whose slot is out of range has c = 0.
+ * Activations are [n][q_len][heads][head_dim] with the given strides in
+ * elements, {entry, token, head}, channels contiguous; any alignment of at
+ * least one element (16-byte aligned pointers and strides load faster).  Rows
+ * j >= c are padding. */
+
+/* Quantise the new tokens' keys and values of one layer into their pages
+ * (q4_sm exactly as qbl_quantize, after NaN -> 0 and clamping to +-32768).
+ * Positions below 0 or without a page are skipped.  qbl_kv_extend comes first:
+ * it makes the pages the slot's own. */
+qbl_status qbl_kv_append(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
+                         int32_t n, int32_t q_len, const void* k, const int64_t k_strides[3], const void* v,
+                         const int64_t v_strides[3], int32_t dtype, void* stream);
+
+/* The values that the cache holds for those tokens, float32, contiguous
+ * [n][q_len][n_kv_heads][head_dim]; 0 in padding rows and where there is no page. */
+qbl_status qbl_kv_read(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
+                       int32_t n, int32_t q_len, float* k_out, float* v_out, void* stream);
+
+/* ------------------------------------------------------------ attention --- */
+
+/* Workspace of qbl_kv_attend for these sizes (may be 0). */
+qbl_status qbl_kv_attend_ws_bytes(const qbl_kv* kv, int32_t n, int32_t q_len, int32_t n_heads, int32_t dtype,
+                                  int64_t max_len, int64_t window, int64_t sinks, int64_t* bytes_out);
+
+/* out = softmax(scale * q K^T) V over the 4-bit cache of one layer, query head
+ * h reading key/value head h / (n_heads / n_kv_heads).
+ *   The query of token j sits at position i = lens[slot] - c + j and sees key t
+ *   iff t <= i and (window == 0 or i - t < window or t < sinks).
+ * q and out: n_heads heads, same dtype (must not overlap); scale 0 means
+ * 1/sqrt(head_dim).  max_len bounds the lengths in use: tokens at positions >=
+ * max_len are not read (keys) and queries there are padding.  Rows that see
+ * nothing (padding, an empty slot, no page) are 0.  Keys without a page are
+ * hidden; what the store holds in hidden places does not matter.
+ * Arithmetic: codes enter the matrix cores exactly.  float32: q and the
+ * weights as three bf16 parts (24 bits), block steps and minima applied in
+ * float32; f16/bf16: see the kernels.  Sums and softmax statistics are
+ * float32.  Deterministic. */
+qbl_status qbl_kv_attend(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
+                         int32_t n, int32_t q_len, int32_t n_heads, const void* q, const int64_t q_strides[3],
+                         void* out, const int64_t out_strides[3], int32_t dtype, int64_t max_len,
+                         int64_t window, int64_t sinks, float scale, void* ws, int64_t ws_bytes, void* stream);
+
+/* ------------------------------------------------ drafted tokens --------- */
+
+/* Workspace of qbl_verify. */
+qbl_status qbl_verify_ws_bytes(int32_t n, int32_t vocab, int64_t* bytes_out);
+
+/* Verify drafted tokens against the target's probabilities from given random
+ * numbers.  Request b has c = counts[b] drafted tokens (NULL: q_len; clamped to
+ * 0..q_len), target rows p_0..p_c and draft rows q_0..q_{c-1}:
+ *   accepted = the first j < c with not (u[b][j] * q_j(x_j) < p_j(x_j)), or c;
+ *   next     = the smallest token t with w(t) > 0 and sum_{s<=t} w(s) >
+ *              u[b][q_len] * sum w (the last with w > 0 if there is none), where
+ *              w = max(p_a - q_a, 0) after a rejection at a (p_a if that is 0
+ *              everywhere) and w = p_c when all c were accepted; -1 if w is 0
+ *              everywhere.
+ * This leaves the target's distribution exact for uniform u.  A probability
+ * that is negative, NaN or infinite counts as 0; rows need not be normalised; a
+ * drafted token outside 0..vocab-1 is rejected.  Products and sums are float64.
+ * target: [n][q_len + 1][vocab], draft: [n][q_len][vocab] or NULL (a
+ * deterministic draft: q = 1 at the drafted token), both of dtype with
+ * {request, row} strides in elements, vocab contiguous; tokens: int32
+ * [n][q_len] (NULL iff q_len = 0); u: float32 [n][q_len + 1]; accepted, next:
+ * int32 [n]. */
+qbl_status qbl_verify(const void* target, const int64_t target_strides[2], const void* draft,
+                      const int64_t draft_strides[2], int32_t dtype, const int32_t* tokens,
+                      const int32_t* counts, const float* u, int32_t n, int32_t q_len, int32_t vocab,
+                      int32_t* accepted, int32_t* next, void* ws, int64_t ws_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* QBL_CACHE_H */

@@ -414,3 +414,6 @@ for _name in dir(Library):
 
 def library_path() -> str:
     return _SO
+
+
+from . import cache  # noqa: E402  (uses the names above)

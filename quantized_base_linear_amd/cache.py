@@ -1,0 +1,257 @@
+"""Python binding of include/qbl_cache.h: the paged 4-bit key/value cache, attention over it (full, or
+with a sliding window and sinks) and the verification of drafted tokens.
+
+Argument marshalling only, as in the package's other functions: they carry the C names, device
+buffers are torch CUDA tensors, outputs and workspaces are the caller's, and the stream defaults to
+torch's current one.  A decode step over drafted tokens reads
+
+    qbl_kv_extend(kv, slots, counts, ws)                        # pages for the new tokens
+    for layer in ...:
+        qbl_kv_append(kv, layer, slots, counts, k, v)           # quantise them into the pages
+        qbl_kv_attend(kv, layer, slots, counts, q, out, max_len, ws=ws2)
+    qbl_verify(target, draft, tokens, counts, u, accepted, next_token, ws3)
+    qbl_kv_truncate(kv, slots, new_lens)                        # drop what was rejected
+
+with every length and count in device memory, so the step needs no host round trip.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _SO, QblError, _dev_ptr, _stream, _ws
+
+QBL_T_F32, QBL_T_F16, QBL_T_BF16 = 0, 1, 2
+QBL_KV_MAX_ENTRIES = 1024
+QBL_KV_MAX_TOKENS = 1 << 24
+QBL_KV_MAX_DRAFT = 256
+DTYPES = {torch.float32: QBL_T_F32, torch.float16: QBL_T_F16, torch.bfloat16: QBL_T_BF16}
+
+
+class qbl_kv(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("n_layers", "n_pages", "page_tokens", "n_kv_heads", "head_dim", "n_slots",
+                                              "max_pages", "reserved")] + \
+               [(f, ctypes.c_void_p) for f in ("store", "refs", "lens", "table", "status")]
+
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+EXPORTS = {
+    "qbl_last_error": (ctypes.c_char_p, []),
+    "qbl_kv_page_bytes": (_i64, [_i32, _i32, _i32]),
+    "qbl_kv_pages_ws_bytes": (_i32, [_vp, _i32, _vp]),
+    "qbl_kv_extend": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _vp]),
+    "qbl_kv_fork": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp]),
+    "qbl_kv_truncate": (_i32, [_vp, _vp, _vp, _i32, _vp]),
+    "qbl_kv_compact": (_i32, [_vp, _vp, _i64, _vp]),
+    "qbl_kv_copy": (_i32, [_vp, _vp, _vp, _i32, _vp]),
+    "qbl_kv_append": (_i32, [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp]),
+    "qbl_kv_read": (_i32, [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
+    "qbl_kv_attend_ws_bytes": (_i32, [_vp, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _vp]),
+    "qbl_kv_attend": (_i32, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                             ctypes.c_float, _vp, _i64, _vp]),
+    "qbl_verify_ws_bytes": (_i32, [_i32, _i32, _vp]),
+    "qbl_verify": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
+}
+_lib = ctypes.CDLL(_SO)
+for _name, (_res, _args) in EXPORTS.items():
+    getattr(_lib, _name).restype = _res
+    getattr(_lib, _name).argtypes = _args
+
+
+def _check(status: int) -> None:
+    if status != 0:
+        raise QblError(status, _lib.qbl_last_error().decode(errors="replace"))
+
+
+class KVCache:
+    """A cache's device tensors and shape.  Tensors that are not given are allocated, empty; given
+    ones are used as they are (store: uint8, the others int32, contiguous)."""
+
+    def __init__(self, n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, n_slots: int,
+                 max_pages: int, device="cuda", store=None, refs=None, lens=None, table=None, status=None):
+        page = qbl_kv_page_bytes(page_tokens, n_kv_heads, head_dim)
+        if page == 0:
+            raise ValueError(f"unsupported page: {page_tokens} tokens, {n_kv_heads} heads of {head_dim} channels")
+
+        def tensor(t, numel, dtype, fill):
+            if t is None:
+                return torch.empty(numel, dtype=dtype, device=device) if fill is None else \
+                    torch.full((numel,), fill, dtype=dtype, device=device)
+            if t.dtype != dtype or t.numel() != numel:
+                raise ValueError(f"expected {numel} elements of {dtype}, got {t.numel()} of {t.dtype}")
+            _dev_ptr(t)
+            return t
+
+        self.n_layers, self.n_pages, self.page_tokens = n_layers, n_pages, page_tokens
+        self.n_kv_heads, self.head_dim, self.n_slots, self.max_pages = n_kv_heads, head_dim, n_slots, max_pages
+        self.store = tensor(store, n_layers * n_pages * page, torch.uint8, None)
+        self.refs = tensor(refs, n_pages, torch.int32, 0)
+        self.lens = tensor(lens, n_slots, torch.int32, 0)
+        self.table = tensor(table, n_slots * max_pages, torch.int32, -1).view(n_slots, max_pages)
+        self.status = tensor(status, 1, torch.int32, 0)
+        self._c = qbl_kv(n_layers, n_pages, page_tokens, n_kv_heads, head_dim, n_slots, max_pages, 0,
+                         self.store.data_ptr(), self.refs.data_ptr(), self.lens.data_ptr(), self.table.data_ptr(),
+                         self.status.data_ptr())
+        self.ptr = ctypes.addressof(self._c)
+
+    def check(self) -> None:
+        """Raises QblError if a page call since the last check could not be done (waits for the device)."""
+        code = int(self.status.item())
+        if code:
+            self.status.zero_()
+            raise QblError(code, "a page call could not be done; it changed nothing")
+
+
+def _ints(t, numel, what):
+    if t is None:
+        return None
+    if t.numel() != numel:
+        raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
+    return _dev_ptr(t, torch.int32)
+
+
+def _strided(t, shape, what):
+    """Data pointer and strides of an activation tensor whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), (_i64 * 3)(*t.stride()[:-1])
+
+
+def _dtype(t):
+    if t.dtype not in DTYPES:
+        raise ValueError(f"unsupported element type {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _bytes(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+# -- pages -----------------------------------------------------------------------------
+def qbl_kv_page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(_lib.qbl_kv_page_bytes(page_tokens, n_kv_heads, head_dim))
+
+
+def qbl_kv_pages_ws_bytes(kv: KVCache, n: int) -> int:
+    out = _i64()
+    _check(_lib.qbl_kv_pages_ws_bytes(kv.ptr, n, ctypes.addressof(out)))
+    return out.value
+
+
+def pages_workspace(kv: KVCache, n: int):
+    """A workspace for qbl_kv_extend and qbl_kv_compact calls of up to n entries."""
+    return _bytes(qbl_kv_pages_ws_bytes(kv, n), kv.store.device)
+
+
+def qbl_kv_extend(kv: KVCache, slots, counts, ws, stream=None) -> None:
+    n = counts.numel()
+    wp, wb = _ws(ws)
+    _check(_lib.qbl_kv_extend(kv.ptr, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, wp, wb, _stream(stream)))
+
+
+def qbl_kv_fork(kv: KVCache, src, dst, prefix=None, stream=None) -> None:
+    n = dst.numel()
+    _check(_lib.qbl_kv_fork(kv.ptr, _ints(src, n, "src"), _ints(dst, n, "dst"), _ints(prefix, n, "prefix"), n,
+                            _stream(stream)))
+
+
+def qbl_kv_truncate(kv: KVCache, slots, new_lens, stream=None) -> None:
+    n = new_lens.numel()
+    _check(_lib.qbl_kv_truncate(kv.ptr, _ints(slots, n, "slots"), _ints(new_lens, n, "new_lens"), n, _stream(stream)))
+
+
+def qbl_kv_compact(kv: KVCache, ws, stream=None) -> None:
+    wp, wb = _ws(ws)
+    _check(_lib.qbl_kv_compact(kv.ptr, wp, wb, _stream(stream)))
+
+
+def qbl_kv_copy(kv: KVCache, src, dst, stream=None) -> None:
+    n = dst.numel()
+    _check(_lib.qbl_kv_copy(kv.ptr, _ints(src, n, "src"), _ints(dst, n, "dst"), n, _stream(stream)))
+
+
+# -- contents --------------------------------------------------------------------------
+def qbl_kv_append(kv: KVCache, layer: int, slots, counts, k, v, stream=None) -> None:
+    """k, v: [n][q_len][n_kv_heads][head_dim], float32, float16 or bfloat16."""
+    n, q_len = k.shape[0], k.shape[1]
+    shape = (n, q_len, kv.n_kv_heads, kv.head_dim)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have one element type")
+    kp, ks = _strided(k, shape, "k")
+    vp, vs = _strided(v, shape, "v")
+    _check(_lib.qbl_kv_append(kv.ptr, layer, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, q_len, kp,
+                              ctypes.addressof(ks), vp, ctypes.addressof(vs), _dtype(k), _stream(stream)))
+
+
+def qbl_kv_read(kv: KVCache, layer: int, slots, counts, k_out, v_out, stream=None) -> None:
+    """k_out, v_out: float32 [n][q_len][n_kv_heads][head_dim], contiguous."""
+    n, q_len = k_out.shape[0], k_out.shape[1]
+    for t in (k_out, v_out):
+        if tuple(t.shape) != (n, q_len, kv.n_kv_heads, kv.head_dim):
+            raise ValueError(f"outputs must be {(n, q_len, kv.n_kv_heads, kv.head_dim)}")
+    _check(_lib.qbl_kv_read(kv.ptr, layer, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, q_len,
+                            _dev_ptr(k_out, torch.float32), _dev_ptr(v_out, torch.float32), _stream(stream)))
+
+
+# -- attention -------------------------------------------------------------------------
+def qbl_kv_attend_ws_bytes(kv: KVCache, n: int, q_len: int, n_heads: int, max_len: int, window: int = 0,
+                           sinks: int = 0, dtype=torch.float32) -> int:
+    out = _i64()
+    _check(_lib.qbl_kv_attend_ws_bytes(kv.ptr, n, q_len, n_heads, DTYPES[dtype], max_len, window, sinks,
+                                       ctypes.addressof(out)))
+    return out.value
+
+
+def attend_workspace(kv: KVCache, n: int, q_len: int, n_heads: int, max_len: int, window: int = 0, sinks: int = 0,
+                     dtype=torch.float32):
+    """A workspace for qbl_kv_attend calls of these sizes (None if they need none)."""
+    return _bytes(qbl_kv_attend_ws_bytes(kv, n, q_len, n_heads, max_len, window, sinks, dtype), kv.store.device)
+
+
+def qbl_kv_attend(kv: KVCache, layer: int, slots, counts, q, out, max_len: int, window: int = 0, sinks: int = 0,
+                  scale: float = 0.0, ws=None, stream=None) -> None:
+    """q, out: [n][q_len][n_heads][head_dim], one element type; scale 0 means 1/sqrt(head_dim)."""
+    n, q_len, heads = q.shape[0], q.shape[1], q.shape[2]
+    shape = (n, q_len, heads, kv.head_dim)
+    if q.dtype != out.dtype:
+        raise ValueError("q and out must have one element type")
+    qp, qs = _strided(q, shape, "q")
+    op, os_ = _strided(out, shape, "out")
+    wp, wb = _ws(ws)
+    _check(_lib.qbl_kv_attend(kv.ptr, layer, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, q_len, heads, qp,
+                              ctypes.addressof(qs), op, ctypes.addressof(os_), _dtype(q), max_len, window, sinks, scale,
+                              wp, wb, _stream(stream)))
+
+
+# -- drafted tokens --------------------------------------------------------------------
+def qbl_verify_ws_bytes(n: int, vocab: int) -> int:
+    out = _i64()
+    _check(_lib.qbl_verify_ws_bytes(n, vocab, ctypes.addressof(out)))
+    return out.value
+
+
+def verify_workspace(n: int, vocab: int, device="cuda"):
+    """A workspace for qbl_verify calls of these sizes."""
+    return _bytes(qbl_verify_ws_bytes(n, vocab), device)
+
+
+def qbl_verify(target, draft, tokens, counts, u, accepted, next_token, ws, stream=None) -> None:
+    """target: [n][q_len + 1][vocab] probabilities, draft: [n][q_len][vocab] or None, tokens: int32
+    [n][q_len] (None if q_len is 0), u: float32 [n][q_len + 1]; accepted, next_token: int32 [n]."""
+    n, q_len, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
+    tp, ts = _strided(target, (n, q_len + 1, vocab), "target")
+    dp, ds = (None, (_i64 * 3)(0, 0, 0)) if draft is None else _strided(draft, (n, q_len, vocab), "draft")
+    if draft is not None and draft.dtype != target.dtype:
+        raise ValueError("target and draft must have one element type")
+    if u.numel() != n * (q_len + 1):
+        raise ValueError(f"u: expected {n * (q_len + 1)} elements, got {u.numel()}")
+    wp, wb = _ws(ws)
+    _check(_lib.qbl_verify(tp, ctypes.addressof(ts), dp, ctypes.addressof(ds), _dtype(target),
+                           _ints(tokens, n * q_len, "tokens"), _ints(counts, n, "counts"), _dev_ptr(u, torch.float32), n,
+                           q_len, vocab, _ints(accepted, n, "accepted"), _ints(next_token, n, "next_token"), wp, wb,
+                           _stream(stream)))

@@ -1,0 +1,358 @@
+// The C ABI of include/qbl_cache.h: argument checks and launch planning of the
+// cache, attention and draft verification calls.  Nothing here reads device
+// memory: what the host cannot see, the kernels check.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <exception>
+
+#include "../../include/qbl_cache.h"
+#include "qbl_cache_kernels.h"
+#include "qbl_host.h"
+
+namespace {
+
+qbl_status fail(qbl_status code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  qbl::set_error(buf);
+  return code;
+}
+
+qbl_status done(hipError_t e, const char* what) {
+  return e == hipSuccess ? QBL_OK : fail(QBL_E_DEVICE, "%s: %s", what, hipGetErrorString(e));
+}
+
+#define CHECK(call)                          \
+  do {                                       \
+    const qbl_status st_ = (call);           \
+    if (st_ != QBL_OK) return st_;           \
+  } while (0)
+
+// The library's boundary: no exception leaves it.
+#define GUARD(...)                                            \
+  try {                                                       \
+    __VA_ARGS__                                               \
+  } catch (const std::exception&) {                           \
+    return QBL_E_NOMEM; /* only the error text can allocate */ \
+  }
+
+bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+qbl_status check_shape(const qbl_kv* kv) {
+  if (!kv) return fail(QBL_E_ARG, "null cache");
+  if (kv->reserved != 0) return fail(QBL_E_ARG, "reserved field must be 0");
+  if (qbl_kv_page_bytes(kv->page_tokens, kv->n_kv_heads, kv->head_dim) == 0)
+    return fail(QBL_E_SHAPE, "unsupported page of %d tokens, %d heads of %d channels", kv->page_tokens, kv->n_kv_heads,
+                kv->head_dim);
+  if (kv->n_layers < 1 || kv->n_pages < 1 || kv->n_slots < 1 || kv->max_pages < 1)
+    return fail(QBL_E_SHAPE, "layers %d, pages %d, slots %d and pages per slot %d must be positive", kv->n_layers,
+                kv->n_pages, kv->n_slots, kv->max_pages);
+  if ((int64_t)kv->max_pages * kv->page_tokens > QBL_KV_MAX_TOKENS)
+    return fail(QBL_E_LIMIT, "%d pages of %d tokens per slot: more than %d tokens", kv->max_pages, kv->page_tokens,
+                QBL_KV_MAX_TOKENS);
+  if (kv->n_pages > 1 << 26 || kv->n_layers > 1 << 16 || kv->n_slots > 1 << 24)
+    return fail(QBL_E_LIMIT, "layers %d, pages %d or slots %d too many", kv->n_layers, kv->n_pages, kv->n_slots);
+  return QBL_OK;
+}
+
+qbl_status check_cache(const qbl_kv* kv) {
+  CHECK(check_shape(kv));
+  if (!kv->store || !kv->refs || !kv->lens || !kv->table || !kv->status) return fail(QBL_E_ARG, "null cache array");
+  if (!aligned(kv->store, 16)) return fail(QBL_E_ARG, "the store must be 16-byte aligned");
+  if (!aligned(kv->refs, 4) || !aligned(kv->lens, 4) || !aligned(kv->table, 4) || !aligned(kv->status, 4))
+    return fail(QBL_E_ARG, "the cache's int32 arrays must be 4-byte aligned");
+  return QBL_OK;
+}
+
+qbl_status check_entries(int32_t n) {
+  if (n < 1) return fail(QBL_E_ARG, "%d entries; need at least one", n);
+  if (n > QBL_KV_MAX_ENTRIES) return fail(QBL_E_LIMIT, "%d entries; at most %d", n, QBL_KV_MAX_ENTRIES);
+  return QBL_OK;
+}
+
+qbl_status check_rows(const qbl_kv* kv, int32_t layer, const int32_t* slots, int32_t n, int32_t q_len) {
+  CHECK(check_cache(kv));
+  if (layer < 0 || layer >= kv->n_layers) return fail(QBL_E_ARG, "layer %d outside 0..%d", layer, kv->n_layers - 1);
+  if (n < 1 || q_len < 1) return fail(QBL_E_ARG, "%d entries of %d tokens; need at least one", n, q_len);
+  if (n > 65535 || q_len > 1 << 20) return fail(QBL_E_LIMIT, "%d entries of %d tokens are too many", n, q_len);
+  if (!slots && n > kv->n_slots) return fail(QBL_E_ARG, "%d entries without slots; the cache has %d", n, kv->n_slots);
+  return QBL_OK;
+}
+
+int64_t elem_bytes(int32_t dtype) { return dtype == QBL_T_F32 ? 4 : 2; }
+
+qbl_status check_type(int32_t dtype) {
+  if (dtype != QBL_T_F32 && dtype != QBL_T_F16 && dtype != QBL_T_BF16)
+    return fail(QBL_E_FORMAT, "unknown element type %d", dtype);
+  return QBL_OK;
+}
+
+// Activation rows: the pointer aligned to its type and strides that keep
+// addresses within 2^62 bytes.
+qbl_status check_array(const void* p, const int64_t* strides, int n_strides, int32_t dtype, const char* what) {
+  if (!p || !strides) return fail(QBL_E_ARG, "null %s", what);
+  if (!aligned(p, (uintptr_t)elem_bytes(dtype))) return fail(QBL_E_ARG, "%s is not aligned to its type", what);
+  for (int i = 0; i < n_strides; ++i)
+    if (strides[i] < 0 || strides[i] > (int64_t)1 << 40)
+      return fail(QBL_E_SHAPE, "%s: stride %lld out of range", what, (long long)strides[i]);
+  return QBL_OK;
+}
+
+bool rows_vectorise(const void* p, const int64_t* strides, int32_t dtype) {
+  const int64_t per = 16 / elem_bytes(dtype);
+  return aligned(p, 16) && strides[0] % per == 0 && strides[1] % per == 0 && strides[2] % per == 0;
+}
+
+qbl_status check_ws(const void* ws, int64_t have, int64_t need) {
+  if (need == 0) return QBL_OK;
+  if (!ws) return fail(QBL_E_ARG, "null workspace; need %lld bytes", (long long)need);
+  if (!aligned(ws, 16)) return fail(QBL_E_ARG, "the workspace must be 16-byte aligned");
+  if (have < need) return fail(QBL_E_BUDGET, "workspace of %lld bytes; need %lld", (long long)have, (long long)need);
+  return QBL_OK;
+}
+
+int64_t round4(int64_t v) { return (v + 3) / 4 * 4; }
+
+// Copy pairs: one per entry (extend), at most half the pages (compact).
+int64_t pages_ws_words(const qbl_kv* kv, int32_t n) {
+  return 4 + 3 * round4(kv->n_pages) + 2 * round4(n > kv->n_pages ? n : kv->n_pages);
+}
+
+qbl::PagesWs pages_ws(const qbl_kv* kv, int32_t n, void* ws) {
+  int32_t* p = static_cast<int32_t*>(ws);
+  qbl::PagesWs w;
+  w.head = p;
+  p += 4;
+  w.a = p;
+  p += round4(kv->n_pages);
+  w.b = p;
+  p += round4(kv->n_pages);
+  w.map = p;
+  p += round4(kv->n_pages);
+  w.src = p;
+  w.dst = p + round4(n > kv->n_pages ? n : kv->n_pages);
+  return w;
+}
+
+qbl::LaunchCtx on(void* stream) {
+  qbl::LaunchCtx lc;
+  lc.stream = static_cast<hipStream_t>(stream);
+  return lc;
+}
+
+// Everything of an attention call that sizes decide.
+qbl_status attend_sizes(const qbl_kv* kv, int32_t n, int32_t q_len, int32_t n_heads, int32_t dtype, int64_t max_len,
+                        int64_t window, int64_t sinks, qbl::KvAttend& a) {
+  CHECK(check_shape(kv));
+  CHECK(check_type(dtype));
+  if (n < 1 || q_len < 1) return fail(QBL_E_ARG, "%d entries of %d tokens; need at least one", n, q_len);
+  if (n > 65535 || q_len > 1 << 20) return fail(QBL_E_LIMIT, "%d entries of %d tokens are too many", n, q_len);
+  if (n_heads < 1 || n_heads % kv->n_kv_heads || n_heads > 1 << 16)
+    return fail(QBL_E_SHAPE, "%d query heads over %d key/value heads", n_heads, kv->n_kv_heads);
+  if (max_len < 1 || max_len > QBL_KV_MAX_TOKENS)
+    return fail(QBL_E_ARG, "max_len %lld outside 1..%d", (long long)max_len, QBL_KV_MAX_TOKENS);
+  if (window < 0 || sinks < 0) return fail(QBL_E_ARG, "negative window or sinks");
+  if ((int64_t)q_len * n_heads > (int64_t)1 << 30 || (int64_t)n * q_len * n_heads > (int64_t)1 << 30)
+    return fail(QBL_E_LIMIT, "%d entries of %d tokens and %d heads are too many rows", n, q_len, n_heads);
+  a.kv = *kv;
+  a.rows.n = n;
+  a.rows.q_len = q_len;
+  a.heads = n_heads;
+  a.group = n_heads / kv->n_kv_heads;
+  a.dtype = dtype;
+  a.max_len = max_len;
+  // positions are below 2^24, so larger values mean the same
+  a.window = window < QBL_KV_MAX_TOKENS ? window : 0;
+  a.sinks = sinks < QBL_KV_MAX_TOKENS ? sinks : QBL_KV_MAX_TOKENS;
+  const qbl::AttendPlan p = qbl::attend_plan(a);
+  if ((int64_t)n * kv->n_kv_heads * p.row_blocks * p.splits >= (int64_t)1 << 31)
+    return fail(QBL_E_LIMIT, "%d entries of %d tokens and %d heads need too many workgroups", n, q_len, n_heads);
+  return QBL_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t qbl_kv_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim) {
+  if (page_tokens != 32 && page_tokens != 64 && page_tokens != 128 && page_tokens != 256) return 0;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  if (n_kv_heads < 1 || n_kv_heads > 1024) return 0;
+  return qbl::kv_tile_bytes(head_dim) * (page_tokens / qbl::kTileTokens) * n_kv_heads;
+}
+
+extern "C" qbl_status qbl_kv_pages_ws_bytes(const qbl_kv* kv, int32_t n, int64_t* bytes_out) {
+  GUARD(
+    CHECK(check_shape(kv));
+    if (!bytes_out) return fail(QBL_E_ARG, "null pointer");
+    if (n < 0) return fail(QBL_E_ARG, "negative entry count");
+    if (n > QBL_KV_MAX_ENTRIES) return fail(QBL_E_LIMIT, "%d entries; at most %d", n, QBL_KV_MAX_ENTRIES);
+    *bytes_out = 4 * pages_ws_words(kv, n);
+    return QBL_OK;
+  )
+}
+
+extern "C" qbl_status qbl_kv_extend(const qbl_kv* kv, const int32_t* slots, const int32_t* counts, int32_t n, void* ws,
+                                    int64_t ws_bytes, void* stream) {
+  GUARD(
+    CHECK(check_cache(kv));
+    CHECK(check_entries(n));
+    if (!counts) return fail(QBL_E_ARG, "null counts");
+    CHECK(check_ws(ws, ws_bytes, 4 * pages_ws_words(kv, n)));
+    return done(qbl::launch_kv_extend(*kv, slots, counts, n, pages_ws(kv, n, ws), on(stream)), "extend launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_fork(const qbl_kv* kv, const int32_t* src, const int32_t* dst, const int32_t* prefix,
+                                  int32_t n, void* stream) {
+  GUARD(
+    CHECK(check_cache(kv));
+    CHECK(check_entries(n));
+    if (!src || !dst) return fail(QBL_E_ARG, "null src or dst");
+    return done(qbl::launch_kv_fork(*kv, src, dst, prefix, n, on(stream)), "fork launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_truncate(const qbl_kv* kv, const int32_t* slots, const int32_t* new_lens, int32_t n,
+                                      void* stream) {
+  GUARD(
+    CHECK(check_cache(kv));
+    CHECK(check_entries(n));
+    if (!new_lens) return fail(QBL_E_ARG, "null new_lens");
+    return done(qbl::launch_kv_truncate(*kv, slots, new_lens, n, on(stream)), "truncate launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_compact(const qbl_kv* kv, void* ws, int64_t ws_bytes, void* stream) {
+  GUARD(
+    CHECK(check_cache(kv));
+    CHECK(check_ws(ws, ws_bytes, 4 * pages_ws_words(kv, 0)));
+    return done(qbl::launch_kv_compact(*kv, pages_ws(kv, 0, ws), on(stream)), "compact launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_copy(const qbl_kv* kv, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {
+  GUARD(
+    CHECK(check_cache(kv));
+    if (n < 1) return fail(QBL_E_ARG, "%d pages; need at least one", n);
+    if (!src || !dst) return fail(QBL_E_ARG, "null src or dst");
+    return done(qbl::launch_kv_copy(*kv, src, dst, nullptr, n, on(stream)), "copy launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_append(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
+                                    int32_t n, int32_t q_len, const void* k, const int64_t k_strides[3], const void* v,
+                                    const int64_t v_strides[3], int32_t dtype, void* stream) {
+  GUARD(
+    CHECK(check_rows(kv, layer, slots, n, q_len));
+    CHECK(check_type(dtype));
+    CHECK(check_array(k, k_strides, 3, dtype, "k"));
+    CHECK(check_array(v, v_strides, 3, dtype, "v"));
+    qbl::KvAppend a;
+    a.kv = *kv;
+    a.layer = layer;
+    a.rows = qbl::KvRows{slots, counts, n, q_len};
+    a.k = k;
+    a.v = v;
+    for (int i = 0; i < 3; ++i) a.ks[i] = k_strides[i], a.vs[i] = v_strides[i];
+    a.dtype = dtype;
+    a.vec = rows_vectorise(k, k_strides, dtype) && rows_vectorise(v, v_strides, dtype);
+    return done(qbl::launch_kv_append(a, on(stream)), "append launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_read(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
+                                  int32_t n, int32_t q_len, float* k_out, float* v_out, void* stream) {
+  GUARD(
+    CHECK(check_rows(kv, layer, slots, n, q_len));
+    if (!k_out || !v_out) return fail(QBL_E_ARG, "null output");
+    if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(QBL_E_ARG, "outputs must be 16-byte aligned");
+    return done(qbl::launch_kv_read(*kv, layer, qbl::KvRows{slots, counts, n, q_len}, k_out, v_out, on(stream)),
+                "read launch");
+  )
+}
+
+extern "C" qbl_status qbl_kv_attend_ws_bytes(const qbl_kv* kv, int32_t n, int32_t q_len, int32_t n_heads, int32_t dtype,
+                                             int64_t max_len, int64_t window, int64_t sinks, int64_t* bytes_out) {
+  GUARD(
+    qbl::KvAttend a{};
+    CHECK(attend_sizes(kv, n, q_len, n_heads, dtype, max_len, window, sinks, a));
+    if (!bytes_out) return fail(QBL_E_ARG, "null pointer");
+    *bytes_out = qbl::attend_plan(a).ws_bytes;
+    return QBL_OK;
+  )
+}
+
+extern "C" qbl_status qbl_kv_attend(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
+                                    int32_t n, int32_t q_len, int32_t n_heads, const void* q, const int64_t q_strides[3],
+                                    void* out, const int64_t out_strides[3], int32_t dtype, int64_t max_len,
+                                    int64_t window, int64_t sinks, float scale, void* ws, int64_t ws_bytes,
+                                    void* stream) {
+  GUARD(
+    CHECK(check_rows(kv, layer, slots, n, q_len));
+    qbl::KvAttend a{};
+    CHECK(attend_sizes(kv, n, q_len, n_heads, dtype, max_len, window, sinks, a));
+    CHECK(check_array(q, q_strides, 3, dtype, "q"));
+    CHECK(check_array(out, out_strides, 3, dtype, "out"));
+    if (q == out) return fail(QBL_E_ARG, "q and out must not overlap");
+    if (!std::isfinite(scale)) return fail(QBL_E_NONFINITE, "scale is not finite");
+    const qbl::AttendPlan p = qbl::attend_plan(a);
+    CHECK(check_ws(ws, ws_bytes, p.ws_bytes));
+    a.layer = layer;
+    a.rows = qbl::KvRows{slots, counts, n, q_len};
+    a.q = q;
+    a.out = out;
+    for (int i = 0; i < 3; ++i) a.qs[i] = q_strides[i], a.os[i] = out_strides[i];
+    a.vec = rows_vectorise(q, q_strides, dtype);
+    a.scale = scale == 0.0f ? 1.0f / std::sqrt((float)kv->head_dim) : scale;
+    a.ws = static_cast<float*>(ws);
+    return done(qbl::launch_kv_attend(a, p, on(stream)), "attend launch");
+  )
+}
+
+extern "C" qbl_status qbl_verify_ws_bytes(int32_t n, int32_t vocab, int64_t* bytes_out) {
+  GUARD(
+    if (!bytes_out) return fail(QBL_E_ARG, "null pointer");
+    if (n < 1 || vocab < 1) return fail(QBL_E_ARG, "%d requests over %d tokens; need at least one", n, vocab);
+    if (n > 65535 || vocab > 1 << 28) return fail(QBL_E_LIMIT, "%d requests over %d tokens are too many", n, vocab);
+    *bytes_out = qbl::verify_ws_bytes(n, vocab);
+    return QBL_OK;
+  )
+}
+
+extern "C" qbl_status qbl_verify(const void* target, const int64_t target_strides[2], const void* draft,
+                                 const int64_t draft_strides[2], int32_t dtype, const int32_t* tokens,
+                                 const int32_t* counts, const float* u, int32_t n, int32_t q_len, int32_t vocab,
+                                 int32_t* accepted, int32_t* next, void* ws, int64_t ws_bytes, void* stream) {
+  GUARD(
+    int64_t need = 0;
+    CHECK(qbl_verify_ws_bytes(n, vocab, &need));
+    CHECK(check_type(dtype));
+    if (q_len < 0) return fail(QBL_E_ARG, "negative draft length");
+    if (q_len > QBL_KV_MAX_DRAFT) return fail(QBL_E_LIMIT, "%d drafted tokens; at most %d", q_len, QBL_KV_MAX_DRAFT);
+    CHECK(check_array(target, target_strides, 2, dtype, "target"));
+    if (draft) CHECK(check_array(draft, draft_strides, 2, dtype, "draft"));
+    if (q_len > 0 && !tokens) return fail(QBL_E_ARG, "null tokens");
+    if (!u || !accepted || !next) return fail(QBL_E_ARG, "null u, accepted or next");
+    CHECK(check_ws(ws, ws_bytes, need));
+    qbl::VerifyArgs a{};
+    a.target = target;
+    a.draft = draft;
+    for (int i = 0; i < 2; ++i) a.ts[i] = target_strides[i], a.ds[i] = draft ? draft_strides[i] : 0;
+    a.dtype = dtype;
+    a.tokens = tokens;
+    a.counts = counts;
+    a.u = u;
+    a.n = n;
+    a.q_len = q_len;
+    a.vocab = vocab;
+    a.accepted = accepted;
+    a.next = next;
+    a.ws = static_cast<double*>(ws);
+    return done(qbl::launch_verify(a, on(stream)), "verify launch");
+  )
+}

@@ -1,0 +1,89 @@
+// Launch interface between the host side of the cache operators (qbl_cache.cpp)
+// and their kernels.  Internal to the library: not part of the C ABI.
+#pragma once
+#include <cstdint>
+
+#include "../../include/qbl_cache.h"
+#include "qbl_cache_index.h"
+#include "qbl_kernels.h"
+
+namespace qbl {
+
+// Workspace words of the page calls (int32): [0] copies to do, [1] used pages,
+// then three arrays of `cap` words and the copy list's two of `entries` words.
+struct PagesWs {
+  int32_t* head;
+  int32_t* a;    // extend: the free pages taken; compact: holes
+  int32_t* b;    // compact: movers, last first
+  int32_t* map;  // compact: page -> page
+  int32_t* src;  // pages to copy
+  int32_t* dst;
+};
+
+hipError_t launch_kv_extend(const qbl_kv& kv, const int32_t* slots, const int32_t* counts, int n, const PagesWs& ws,
+                            const LaunchCtx& lc);
+hipError_t launch_kv_fork(const qbl_kv& kv, const int32_t* src, const int32_t* dst, const int32_t* prefix, int n,
+                          const LaunchCtx& lc);
+hipError_t launch_kv_truncate(const qbl_kv& kv, const int32_t* slots, const int32_t* lens, int n,
+                              const LaunchCtx& lc);
+hipError_t launch_kv_compact(const qbl_kv& kv, const PagesWs& ws, const LaunchCtx& lc);
+hipError_t launch_kv_copy(const qbl_kv& kv, const int32_t* src, const int32_t* dst, const int32_t* count, int n,
+                          const LaunchCtx& lc);
+
+struct KvAppend {
+  qbl_kv kv;
+  int layer;
+  KvRows rows;
+  const void* k;
+  const void* v;
+  int64_t ks[3], vs[3];  // strides in elements: entry, token, head
+  int dtype;
+  int vec;               // 1: every row of channels is 16-byte aligned
+};
+hipError_t launch_kv_append(const KvAppend& a, const LaunchCtx& lc);
+hipError_t launch_kv_read(const qbl_kv& kv, int layer, const KvRows& rows, float* k_out, float* v_out,
+                          const LaunchCtx& lc);
+
+struct KvAttend {
+  qbl_kv kv;
+  int layer;
+  KvRows rows;
+  int heads, group;      // query heads; query heads per key/value head
+  const void* q;
+  void* out;
+  int64_t qs[3], os[3];
+  int dtype;
+  int vec;               // 1: every row of q is 16-byte aligned
+  int64_t max_len, window, sinks;
+  float scale;
+  float* ws;             // partial results of the splits (attend_plan)
+};
+// How a call is split: rows of one key/value head per workgroup and tiles of
+// the cache per split.
+struct AttendPlan {
+  int cols;          // query rows per workgroup
+  int row_blocks;    // workgroups along the rows
+  int chunk;         // tiles per split
+  int splits;
+  int64_t ws_bytes;
+};
+AttendPlan attend_plan(const KvAttend& a);
+hipError_t launch_kv_attend(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc);
+
+struct VerifyArgs {
+  const void* target;
+  const void* draft;
+  int64_t ts[2], ds[2];
+  int dtype;
+  const int32_t* tokens;
+  const int32_t* counts;
+  const float* u;
+  int n, q_len, vocab;
+  int32_t* accepted;
+  int32_t* next;
+  double* ws;
+};
+int64_t verify_ws_bytes(int n, int vocab);
+hipError_t launch_verify(const VerifyArgs& a, const LaunchCtx& lc);
+
+}  // namespace qbl

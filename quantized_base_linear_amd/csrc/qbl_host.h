@@ -7,6 +7,9 @@
 
 namespace qbl {
 
+// Sets the calling thread's qbl_last_error() text.
+void set_error(const char* text);
+
 // FIPS 180-4 SHA-256.
 class Sha256 {
  public:

@@ -1,0 +1,213 @@
+// Contents of the paged 4-bit key/value cache: quantise new tokens into their
+// pages, and read tokens back.
+//
+// A block of 32 channels of one token becomes a q4_sm block: m = fp16(min),
+// d = fp16((max - m)/15), code = (x - m)/d rounded half away from zero into
+// 0..15, in float32 with correctly rounded divisions, the steps of the host
+// quantiser, so both give the same bits.  Both kernels move bytes only and are
+// bound by memory (prompts) or by launch latency (single tokens).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "qbl_cache_device.h"
+
+namespace qbl {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kClamp = 32768.0f;  // keeps d*15 + m inside fp16's range
+
+__device__ __forceinline__ float tame(float x) { return x == x ? fminf(fmaxf(x, -kClamp), kClamp) : 0.0f; }
+
+// Quantise 8 of a block's 32 channels; the other 24 are with the three
+// neighbouring lanes (4-lane groups).  Returns the codes as two words of four
+// bytes each (channels 0..3 and 4..7) and the block's d | m << 16.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& lo4, uint32_t& hi4) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = fmaxf(hi, x[j]);
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    lo = fminf(lo, __shfl_xor(lo, s));
+    hi = fmaxf(hi, __shfl_xor(hi, s));
+  }
+  const __half mh = __float2half_rn(lo);
+  const float m = __half2float(mh);
+  const __half dh = __float2half_rn((hi - m) / 15.0f);
+  const float d = __half2float(dh);
+  lo4 = hi4 = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float t = d > 0.0f ? (x[j] - m) / d : 0.0f;
+    t = fminf(fmaxf(t, 0.0f), 15.0f);
+    const float w = floorf(t);
+    const uint32_t code = (uint32_t)w + (t - w >= 0.5f ? 1u : 0u);
+    if (j < 4) lo4 |= code << (8 * j);
+    else hi4 |= code << (8 * (j - 4));
+  }
+  return (uint32_t)__half_as_ushort(dh) | (uint32_t)__half_as_ushort(mh) << 16;
+}
+
+// One workgroup owns one tile (32 tokens) of one head of one entry, so no two
+// write the same byte: the values' codes of 8 tokens share a word, and tokens
+// that the call does not cover keep their nibbles.
+template <int DIM, int T>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend a, int page_shift) {
+  constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4;
+  constexpr int kRow = DIM + 4;                  // bytes; the pad spreads a channel's tokens over the banks
+  __shared__ uint32_t codes[32 * kRow / 4];
+  const qbl_kv& kv = a.kv;
+  const int i = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const Entry e = load_entry(kv, a.rows, i);
+  const int first = max(e.len - e.c, 0);         // positions [first, len) are written
+  const int base = ((first >> 5) + (int)blockIdx.x) << 5;
+  if (e.slot < 0 || e.c == 0 || base >= e.len) return;
+  const int page = page_of(kv, e.slot, base, page_shift);
+  if (page < 0) return;
+  uint8_t* tile = tile_ptr<DIM>(kv, a.layer, page, h, base, page_shift);
+  const int t0 = max(first - base, 0), t1 = min(e.len - base, 32);
+  const int j0 = base - (e.len - e.c);           // row of the tile's token 0
+
+  const int work = (t1 - t0) * kNb * 4;          // (token, block, quad)
+  uint32_t* kc = reinterpret_cast<uint32_t*>(tile);
+  uint32_t* ks = reinterpret_cast<uint32_t*>(tile + 16 * DIM);
+  uint16_t* vs = reinterpret_cast<uint16_t*>(tile + 32 * DIM + 128 * kNb);
+  for (int w0 = 0; w0 < 2 * work; w0 += kThreads) {
+    const int w = w0 + tid;
+    const bool live = w < 2 * work;
+    const bool val = w >= work;
+    const int x = live ? (val ? w - work : w) : 0;
+    const int quad = x & 3, g = (x >> 2) % kNb, t = t0 + (x >> 2) / kNb;
+    float f[8];
+    {
+      const int64_t* st = val ? a.vs : a.ks;
+      const int64_t at = (int64_t)i * st[0] + (int64_t)(j0 + t) * st[1] + (int64_t)h * st[2] + g * 32 + quad * 8;
+      load8<T>(val ? a.v : a.k, at, a.vec, f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = tame(f[j]);
+    uint32_t lo4, hi4;
+    const uint32_t dm = quantise8(f, lo4, hi4);  // every lane takes part in the 4-lane minimum
+    if (!live) continue;
+    if (!val) {
+      kc[((g / kNg * 32 + t) * 4 + quad) * kNg + g % kNg] = lo4 | hi4 << 4;
+      if (quad == 0) ks[t * kNb + g] = dm;
+    } else {
+      codes[(t * kRow + g * 32 + quad * 8) / 4] = lo4;
+      codes[(t * kRow + g * 32 + quad * 8) / 4 + 1] = hi4;
+      if (quad == 0) {
+        const int s = (g * 4 + (t & 15) / 4) * 8 + (t >> 4) * 4 + (t & 3);
+        vs[s] = (uint16_t)dm;
+        vs[32 * kNb + s] = (uint16_t)(dm >> 16);
+      }
+    }
+  }
+  __syncthreads();
+  const uint8_t* cb = reinterpret_cast<const uint8_t*>(codes);
+  uint32_t* vc = reinterpret_cast<uint32_t*>(tile + 16 * DIM + 128 * kNb);
+  for (int w = tid; w < DIM * 4; w += kThreads) {  // word (chunk, lane, quad, n)
+    const int n = w & 3, quad = (w >> 2) & 3, lane = (w >> 4) & 15, chunk = w >> 8;
+    const int ch = chunk * 64 + n * 16 + lane;
+    uint32_t word = 0, mask = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int ta = quad * 4 + j, tb = 16 + ta;
+      if (ta >= t0 && ta < t1) word |= (uint32_t)cb[ta * kRow + ch] << (8 * j), mask |= 0xFu << (8 * j);
+      if (tb >= t0 && tb < t1) word |= (uint32_t)cb[tb * kRow + ch] << (8 * j + 4), mask |= 0xF0u << (8 * j);
+    }
+    if (mask == 0) continue;
+    if (mask != 0xFFFFFFFFu) word |= vc[w] & ~mask;
+    vc[w] = word;
+  }
+}
+
+// One workgroup per 8 rows of one head: a thread per 8 channels of a row.
+template <int DIM>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(qbl_kv kv, int layer, KvRows rows, float* k_out, float* v_out,
+                                                           int page_shift) {
+  constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4;
+  const int h = blockIdx.y, i = blockIdx.z;
+  const Entry e = load_entry(kv, rows, i);
+  constexpr int kPer = DIM / 8;                  // threads per row
+  const int j = blockIdx.x * (kThreads / kPer) + threadIdx.x / kPer;
+  if (j >= rows.q_len) return;
+  const int part = threadIdx.x % kPer, quad = part & 3, g = part >> 2;
+  float kx[8], vx[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) kx[c] = vx[c] = 0.0f;
+  const int pos = e.len - e.c + j;
+  int page = -1;
+  if (j < e.c && pos >= 0) page = page_of(kv, e.slot, pos, page_shift);
+  if (page >= 0) {
+    const uint8_t* tile = tile_ptr<DIM>(kv, layer, page, h, pos, page_shift);
+    const int t = pos & 31;
+    const uint32_t w = reinterpret_cast<const uint32_t*>(tile)[((g / kNg * 32 + t) * 4 + quad) * kNg + g % kNg];
+    const uint32_t dm = reinterpret_cast<const uint32_t*>(tile + 16 * DIM)[t * kNb + g];
+    const uint16_t* vs = reinterpret_cast<const uint16_t*>(tile + 32 * DIM + 128 * kNb);
+    const int s = (g * 4 + (t & 15) / 4) * 8 + (t >> 4) * 4 + (t & 3);
+    const float kd = half_bits(dm & 0xFFFFu), km = half_bits(dm >> 16);
+    const float vd = half_bits(vs[s]), vm = half_bits(vs[32 * kNb + s]);
+    const uint8_t* vc = tile + 16 * DIM + 128 * kNb;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      kx[c] = fmaf(kd, (float)((w >> (8 * (c & 3) + 4 * (c >> 2))) & 15u), km);
+      const int ch = g * 32 + quad * 8 + c;
+      const uint32_t b = vc[(((ch / 64 * 16 + ch % 16) * 4 + (t & 15) / 4) * 4 + ch % 64 / 16) * 4 + (t & 3)];
+      vx[c] = fmaf(vd, (float)((b >> (4 * (t >> 4))) & 15u), vm);
+    }
+  }
+  const int64_t at = (((int64_t)i * rows.q_len + j) * kv.n_kv_heads + h) * DIM + g * 32 + quad * 8;
+  float4* ko = reinterpret_cast<float4*>(k_out + at);
+  float4* vo = reinterpret_cast<float4*>(v_out + at);
+  ko[0] = make_float4(kx[0], kx[1], kx[2], kx[3]);
+  ko[1] = make_float4(kx[4], kx[5], kx[6], kx[7]);
+  vo[0] = make_float4(vx[0], vx[1], vx[2], vx[3]);
+  vo[1] = make_float4(vx[4], vx[5], vx[6], vx[7]);
+}
+
+int page_shift_of(const qbl_kv& kv) { return __builtin_ctz((unsigned)kv.page_tokens); }
+
+template <int DIM>
+hipError_t append_dim(const KvAppend& a, const LaunchCtx& lc) {
+  // new tokens touch at most this many tiles, wherever they start in one
+  const dim3 grid((unsigned)((a.rows.q_len + 30) / 32 + 1), (unsigned)a.kv.n_kv_heads, (unsigned)a.rows.n);
+  const int sh = page_shift_of(a.kv);
+  if (a.dtype == QBL_T_F32) QBL_LAUNCH((kv_append_kernel<DIM, QBL_T_F32>), grid, dim3(kThreads), 0, lc, a, sh);
+  else if (a.dtype == QBL_T_F16) QBL_LAUNCH((kv_append_kernel<DIM, QBL_T_F16>), grid, dim3(kThreads), 0, lc, a, sh);
+  else QBL_LAUNCH((kv_append_kernel<DIM, QBL_T_BF16>), grid, dim3(kThreads), 0, lc, a, sh);
+  return hipGetLastError();
+}
+
+template <int DIM>
+hipError_t read_dim(const qbl_kv& kv, int layer, const KvRows& rows, float* k_out, float* v_out, const LaunchCtx& lc) {
+  constexpr int kRows = kThreads / (DIM / 8);
+  const dim3 grid((unsigned)((rows.q_len + kRows - 1) / kRows), (unsigned)kv.n_kv_heads, (unsigned)rows.n);
+  QBL_LAUNCH(kv_read_kernel<DIM>, grid, dim3(kThreads), 0, lc, kv, layer, rows, k_out, v_out, page_shift_of(kv));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppend& a, const LaunchCtx& lc) {
+  (void)hipGetLastError();  // drop errors left by earlier, unrelated calls
+  switch (a.kv.head_dim) {
+    case 64: return append_dim<64>(a, lc);
+    case 128: return append_dim<128>(a, lc);
+    case 256: return append_dim<256>(a, lc);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_read(const qbl_kv& kv, int layer, const KvRows& rows, float* k_out, float* v_out,
+                          const LaunchCtx& lc) {
+  (void)hipGetLastError();
+  switch (kv.head_dim) {
+    case 64: return read_dim<64>(kv, layer, rows, k_out, v_out, lc);
+    case 128: return read_dim<128>(kv, layer, rows, k_out, v_out, lc);
+    case 256: return read_dim<256>(kv, layer, rows, k_out, v_out, lc);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace qbl

@@ -64,6 +64,8 @@ bool all_finite(const float* p, int64_t n) {
 
 }  // namespace
 
+void qbl::set_error(const char* text) { g_err = text; }
+
 // ----------------------------------------------------------------- objects ---
 
 struct DevLinear {
