@@ -13,7 +13,7 @@ SO = os.path.join(HERE, "libqbl.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["qbl_gemv.hip", "qbl_batched.hip", "qbl_jit.hip", "qbl_dar.hip", "qbl_probe.hip", "qbl_static.hip",
-           "qbl_kv.hip", "qbl_pages.hip", "qbl_attend.hip", "qbl_verify.hip",
+           "qbl_kv.hip", "qbl_pages.hip", "qbl_attend.hip", "qbl_attend_rows.hip", "qbl_verify.hip",
            "qbl_format.cpp", "qbl_runtime.cpp", "qbl_cache.cpp"]
 # Packed fp32 VALU ops are disabled on purpose (the flag only affects device code).
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -1,78 +1,45 @@
-// Attention over the paged 4-bit key/value cache (decode form, any row count).
+// Attention over the paged 4-bit key/value cache for few query rows (decode,
+// drafts, short chunks), the join of split calls, and the plan of a call.
 //
 //   out = softmax(c q K^T) V,  K and V in blocks of 32 channels: x = d*code + m.
 //
-// Both products run on the matrix cores with the integer codes as exact bf16
-// operands, and the block steps and minima enter outside in float32:
-//   score(t, q)  = c * sum_g [ d_K(t,g) * (sum_{k in g} code(t,k) q_k) + m_K(t,g) * sum_{k in g} q_k ]
-//   out(q, c)   ~  sum_t (p_t d_V(t,g)) code(t,c) + sum_t p_t m_V(t,g),   g = c / 32
-// so no key or value is ever rounded.  The other operand is split into bf16
-// parts: hi + mid + lo hold a float32's 24 bits.
+// Both products run on the matrix cores in f16 with float32 sums.
+//   float32 and f16 rows: no key or value is rounded.  With d = dh + dl (7 and
+//   4 significant bits) the products (code - 8)*dh and (code - 8)*dl are exact
+//   f16 numbers, and the rest of a block is linear in its scales:
+//     score(t, q)  = c * [ sum_k (dh + dl)(code - 8) q_k + sum_g (8 d + m)(t,g) * qsum_g ]
+//     out(q, ch)  ~  sum_t p_t (dh + dl)(code - 8) + sum_t p_t (8 d + m)(t,g),  g = ch / 32.
+//   The last terms are matrix products too, whose operands are the scales as
+//   they are stored.  Queries (float32) and weights enter as two f16 parts.
+//   bf16 rows: x is rounded once to f16 (2^-12 relative, against the output's
+//   2^-9), the weights too.
+// Query rows are scaled by a power of two (largest value in [2^6, 2^7)), so
+// that every part fits f16; weights carry 2^11.
 //
 // A workgroup serves one key/value head of one entry: 16 * NT query rows (the
 // query heads that share the head, times the new tokens) against a run of
 // tiles, its four waves taking tiles in turn.  Tokens are the rows of the
 // score product, so its result is already laid out as the second product's
 // operand: lane (quad, row q) holds tokens 4 quad + 0..3 of both halves of the
-// tile, which is the order that the value codes are stored in.  Codes go from
-// global memory straight into operand registers, one tile ahead; only the
-// scales go through LDS, as every lane needs those of 8 tokens.
+// tile, which is the order that the value codes are stored in.  Codes and
+// scales go from global memory straight into registers, one tile ahead; only
+// the values' steps go through LDS, as every lane needs those of 8 tokens.
 //
 // The softmax is one pass: each row keeps a reference maximum that is raised
-// (and the sums rescaled) only when a score passes it by 8 in the exponent of
+// (and the sums rescaled) only when a score passes it by 4 in the exponent of
 // 2, so in most tiles no cross-lane step is needed.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
-#include "qbl_cache_device.h"
+#include "qbl_attend_device.h"
 
 namespace qbl {
 namespace {
 
-typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
-typedef float f4v __attribute__((ext_vector_type(4)));
-
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kNegInf = -__builtin_inff();
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kSlack = 8.0f;  // weights stay below 2^8 times the reference
-
-__device__ __forceinline__ Span block_span(const KvAttend& a, const Entry& e, int r0, int cols) {
-  return row_span(e, r0, cols, a.group, (int)a.max_len, (int)a.window, (int)a.sinks);
-}
-
-// Codes of one word as bf16, in the order channel (or token) 0..7.  A nibble n
-// read as an e4m3 number is n * 2^-9 exactly (subnormal up to 7, then the first
-// binade), and the conversion multiplies by 2^9.
-__device__ __forceinline__ bf8v codes8(uint32_t w) {
-  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-  const bf2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
-  const bf2v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
-  const bf2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
-  const bf2v d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
-  return bf8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// x as P bf16 parts, largest first; the parts of three sum to x exactly up to
-// float32's range ends.
-template <int P>
-__device__ __forceinline__ void split8(const float (&x)[8], bf8v (&part)[P]) {
-  float rest[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) rest[j] = x[j];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) part[p][j] = (__bf16)rest[j];
-    if (p + 1 < P) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) rest[j] -= (float)part[p][j];
-    }
-  }
-}
+constexpr int kMaxSplits = 1024;
 
 // LDS writes of this wave become visible to its own later reads; no other wave takes part.
 __device__ __forceinline__ void wave_sync() {
@@ -84,10 +51,11 @@ __device__ __forceinline__ void wave_sync() {
 template <int DIM>
 struct TileRegs {
   static constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4;
-  uint32_t kc[2][kNb];      // key codes of token 16 s + col
-  uint32_t vc[DIM / 16];    // value codes of channel 16 n + col
-  uint32_t sc[kNb];         // this lane's piece of the scales
-  int pos;                  // first token position, or -1: no page
+  uint32_t kc[2][kNb];   // key codes of token 16 half + col
+  uint32_t ks[2][kNb];   // its scales
+  uint32_t vc[DIM / 16]; // value codes of channel 16 n + col
+  uint4 vs;              // row col of the value scales, tokens of quad
+  int pos;               // first token position, or -1: no page
 };
 
 template <int N>
@@ -102,48 +70,60 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N], 
 }
 
 template <int DIM>
-__device__ __forceinline__ void load_tile(const KvAttend& a, const Entry& e, const Span& s, int h, int v, int page_shift,
+__device__ __forceinline__ void load_tile(const KvAttend& a, const Entry& e, int pos, int page, int h, int page_shift,
                                           int lane, TileRegs<DIM>& t) {
   constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4;
   const int col = lane & 15, quad = lane >> 4;
-  const int pos = __builtin_amdgcn_readfirstlane(span_pos(s, v));
-  const int page = __builtin_amdgcn_readfirstlane(page_of(a.kv, e.slot, pos, page_shift));
   t.pos = page < 0 ? -1 : pos;
+  t.vs = make_uint4(0, 0, 0, 0);
   if (page < 0) {
 #pragma unroll
-    for (int k = 0; k < kNb; ++k) t.kc[0][k] = t.kc[1][k] = t.sc[k] = 0;
+    for (int k = 0; k < kNb; ++k) t.kc[0][k] = t.kc[1][k] = t.ks[0][k] = t.ks[1][k] = 0;
 #pragma unroll
     for (int k = 0; k < DIM / 16; ++k) t.vc[k] = 0;
     return;
   }
   const uint8_t* p = tile_ptr<DIM>(a.kv, a.layer, page, h, pos, page_shift);
   const uint32_t* kc = reinterpret_cast<const uint32_t*>(p);
+  const uint32_t* ks = reinterpret_cast<const uint32_t*>(p + 16 * DIM);
   const uint32_t* vc = reinterpret_cast<const uint32_t*>(p + 16 * DIM + 128 * kNb);
+  const uint4* vs = reinterpret_cast<const uint4*>(p + 32 * DIM + 128 * kNb);
 #pragma unroll
   for (int half = 0; half < 2; ++half)
 #pragma unroll
-    for (int ch = 0; ch < kNb / kNg; ++ch)
+    for (int ch = 0; ch < kNb / kNg; ++ch) {
       load_words<kNb>(kc + ((ch * 32 + half * 16 + col) * 4 + quad) * kNg, t.kc[half], 4 * ch);
+      load_words<kNb>(ks + (half * 16 + col) * kNb + 4 * ch, t.ks[half], 4 * ch);
+    }
+  if (col < 2 * kNb) t.vs = vs[col * 4 + quad];
 #pragma unroll
   for (int ch = 0; ch < DIM / 64; ++ch) load_words<DIM / 16>(vc + ((ch * 16 + col) * 4 + quad) * 4, t.vc, 4 * ch);
-  // lanes 0..31: key scales, 32..63: value scales, kNb words each
-  const uint8_t* sp = p + (lane < 32 ? 16 * DIM : 32 * DIM + 128 * kNb) + (lane & 31) * 4 * kNb;
-#pragma unroll
-  for (int ch = 0; ch < (kNb + 3) / 4; ++ch) load_words<kNb>(reinterpret_cast<const uint32_t*>(sp) + 4 * ch, t.sc, 4 * ch);
 }
+
+// d as dh (7 significant bits) + dl, both halves at a time.
+__device__ __forceinline__ void split_step(uint32_t d, h2v& dh, h2v& dl) {
+  dh = as_h2(d & 0xFFF0FFF0u);
+  dl = as_h2(d) - dh;
+}
+
+__device__ __forceinline__ h2v times8(h2v x) { return x * h2v{(_Float16)8.0f, (_Float16)8.0f}; }
+
+__device__ __forceinline__ f4v mfma(h8v x, h8v y, f4v acc) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, acc, 0, 0, 0); }
 
 template <int DIM, int T, int NT>
 __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_blocks, int chunk, int splits,
                                                           int page_shift, int64_t part_floats) {
   constexpr int kNb = DIM / 32;
-  constexpr int kQp = T == QBL_T_F32 ? 3 : T == QBL_T_F16 ? 2 : 1;  // bf16 parts of q: all of its bits
-  constexpr int kPp = T == QBL_T_F32 ? 3 : 2;                       // bf16 parts of the weights
+  constexpr bool kExact = T != QBL_T_BF16;
+  constexpr int kQp = T == QBL_T_F32 ? 2 : 1;  // f16 parts of q
+  constexpr int kPp = kExact ? 2 : 1;          // f16 parts of the weights
   constexpr int kOut = DIM + 4;
-  __shared__ __align__(16) uint32_t scales[kWaves][64 * kNb];
+  __shared__ uint4 steps[kWaves][8 * kNb];
   __shared__ __align__(16) float obuf[kWaves][16][kOut];
+  __shared__ float linear[kWaves][16][17];
   __shared__ float ml[kWaves][16][2];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
   int b = blockIdx.x;
   const int split = b % splits;
@@ -153,12 +133,22 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
   const int h = b % a.kv.n_kv_heads, i = b / a.kv.n_kv_heads;
   const Entry e = load_entry(a.kv, a.rows, i);
   const int r0 = rb * 16 * NT;
-  const Span sp = block_span(a, e, r0, 16 * NT);
+  const int win = (int)a.window, sinks = (int)a.sinks;
+  const Span sp = row_span(e, r0, 16 * NT, a.group, (int)a.max_len, win, sinks);
   if (splits > 1 && split * chunk >= sp.tiles) return;
+  const int v1 = min(sp.tiles, (split + 1) * chunk);
+  int v = split * chunk + wave;
 
-  bf8v q[NT][kNb][kQp];
-  float qsum[NT][kNb];
-  int pos_of[NT];  // this lane's row's position, -1 for padding
+  auto fetch = [&](int x, TileRegs<DIM>& t) {
+    const int pos = span_pos(sp, x);
+    load_tile<DIM>(a, e, pos, page_of_uniform(a.kv, e.slot, pos, page_shift), h, page_shift, lane, t);
+  };
+  TileRegs<DIM> ta, tb;
+  if (v < v1) fetch(v, ta);
+
+  h8v q[NT][kNb][kQp], qs[NT][kNb / 4 + 1];  // qs: what the blocks' scales (d, m) x 4 meet, part `quad` of 8*qsum, qsum
+  float cs[NT];                              // score factor, in the exponent of 2
+  int pos_of[NT];                            // this lane's row's position, -1 for padding
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = r0 + nt * 16 + col;
@@ -166,160 +156,217 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
     const int pos = e.len - e.c + j;
     const bool ok = r < e.c * a.group && pos >= sp.first && pos <= sp.last;
     pos_of[nt] = ok ? pos : -1;
+    float x[kNb][8], big = 0.0f;
+    const int64_t at = (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] +
+                       (int64_t)(h * a.group + r - j * a.group) * a.qs[2] + quad * 8;
 #pragma unroll
     for (int g = 0; g < kNb; ++g) {
-      float x[8];
-      if (ok) {
-        const int64_t at = (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] +
-                           (int64_t)(h * a.group + r - j * a.group) * a.qs[2] + g * 32 + quad * 8;
-        load8<T>(a.q, at, a.vec, x);
-      } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = 0.0f;
+      for (int k = 0; k < 8; ++k) x[g][k] = 0.0f;
+      if (ok) load8<T>(a.q, at + g * 32, a.vec, x[g]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[g][k]));
+    }
+    const int ex = row_exponent(big, 6);
+    const float up = a.scale < 0.0f ? -pow2(ex) : pow2(ex);
+    cs[nt] = fabsf(a.scale) * kLog2e * pow2(-ex);
+#pragma unroll
+    for (int g = 0; g < kNb; ++g) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[g][k] *= up, sum += x[g][k];
+#pragma unroll
+      for (int p = 0; p < kQp; ++p)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          q[nt][g][p][k] = (_Float16)x[g][k];
+          x[g][k] -= (float)q[nt][g][p][k];
+        }
+      if constexpr (kExact) {
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        // quad 0, 1, 2 hold the first, second and third part; quad 3 none
+        _Float16 part = (_Float16)0.0f;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const _Float16 y = (_Float16)sum;
+          sum -= (float)y;
+          part = quad == p ? y : part;
+        }
+        qs[nt][g / 4][2 * (g % 4)] = part * (_Float16)8.0f;
+        qs[nt][g / 4][2 * (g % 4) + 1] = part;
       }
-      split8<kQp>(x, q[nt][g]);
-      float s = 0.0f;
+    }
+    if constexpr (kExact && kNb == 2) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += x[k];
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      qsum[nt][g] = s;
+      for (int k = 4; k < 8; ++k) qs[nt][0][k] = (_Float16)0.0f;
     }
   }
 
-  f4v o[NT][DIM / 16];
-  float msum[NT][kNb], m[NT], l[NT];
+  f4v o[NT][DIM / 16], lin[NT];
+  float m[NT], l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt] = kNegInf, l[nt] = 0.0f;
+    lin[nt] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int n = 0; n < DIM / 16; ++n) o[nt][n] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int g = 0; g < kNb; ++g) msum[nt][g] = 0.0f;
   }
-  const float c2 = a.scale * kLog2e;
-  const int win = (int)a.window, sinks = (int)a.sinks;
-  const int v1 = min(sp.tiles, (split + 1) * chunk);
-  uint32_t* sc = scales[wave];
+  uint4* sc = steps[wave];
 
-  TileRegs<DIM> t;
-  int v = split * chunk + wave;
-  if (v < v1) load_tile<DIM>(a, e, sp, h, v, page_shift, lane, t);
-  for (; v < v1; v += kWaves) {
+  auto step = [&](TileRegs<DIM>& t, TileRegs<DIM>& next) {
+    if (v + kWaves < v1) fetch(v + kWaves, next);
+    if (t.pos < 0) return;
     const int pos = t.pos;
-    const bool have = pos >= 0;
-    const bool full = have && pos + 31 <= sp.first && (win == 0 || pos >= sp.last - win + 1 || pos + 31 < sinks);
-    if (have && !full && lane >= 32) {
-      // Value scales of tokens that no row sees become 0, so that whatever is
-      // stored there meets a weight of 0 as a finite number.
-#pragma unroll
-      for (int k = 0; k < kNb; ++k) {
-        const int at = (lane & 31) * 2 * kNb + 2 * k;   // half index: [d | m][block][quad][8]
-        const int qd = at >> 3 & 3;
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int x = (at + z) & 7;
-          const int tok = pos + (x >> 2) * 16 + qd * 4 + (x & 3);
-          const bool seen = tok <= sp.last && (win == 0 || tok < sinks || tok > sp.first - win);
-          if (!seen) t.sc[k] &= z ? 0x0000FFFFu : 0xFFFF0000u;
-        }
-      }
-    }
+    const bool full = pos + 31 <= sp.first && (win == 0 || pos >= sp.last - win + 1 || pos + 31 < sinks);
+    // Value scales of tokens that no row sees become 0, so that whatever is
+    // stored there meets a weight of 0 as a finite number.
+    if (!full) t.vs = hide(t.vs, pos, quad, sp, win, sinks);
     wave_sync();
-#pragma unroll
-    for (int k = 0; k < kNb; ++k) sc[lane * kNb + k] = t.sc[k];
+    if (col < 2 * kNb) sc[col * 4 + quad] = t.vs;
     wave_sync();
-    const TileRegs<DIM> cur = t;
-    if (v + kWaves < v1) load_tile<DIM>(a, e, sp, h, v + kWaves, page_shift, lane, t);
-    if (!have) continue;
 
     float s[NT][8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint32_t* dm = sc + (half * 16 + quad * 4) * kNb;
+      f4v acc[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (kExact) {
+#pragma unroll
+        for (int c = 0; c < (kNb + 3) / 4; ++c) {
+          uint4 w = make_uint4(t.ks[half][4 * c], t.ks[half][4 * c + 1], 0, 0);
+          if constexpr (kNb >= 4) w.z = t.ks[half][4 * c + 2], w.w = t.ks[half][4 * c + 3];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(__builtin_bit_cast(h8v, w), qs[nt][c], acc[nt]);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < kNb; ++g) {
+        h2v c[4], x[4];
+        codes8(t.kc[half][g], c);
+        const h2v d = low2(t.ks[half][g]);
+        if constexpr (kExact) {
+          h2v dh, dl;
+          split_step(__builtin_bit_cast(uint32_t, d), dh, dl);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[z] = __builtin_elementwise_fma(c[z], dl, -times8(dl));
+          const h8v lo = join8(x);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[z] = __builtin_elementwise_fma(c[z], dh, -times8(dh));
+          const h8v hi = join8(x);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int p = kQp - 1; p >= 0; --p) acc[nt] = mfma(hi, q[nt][g][p], mfma(lo, q[nt][g][p], acc[nt]));
+        } else {
+          const h2v mm = high2(t.ks[half][g]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[z] = __builtin_elementwise_fma(c[z], d, mm);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(join8(x), q[nt][g][0], acc[nt]);
+        }
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[nt][half * 4 + r] = 0.0f;
-#pragma unroll
-      for (int g = 0; g < kNb; ++g) {
-        const bf8v kc = codes8(cur.kc[half][g]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          f4v d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int p = kQp - 1; p >= 0; --p) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc, q[nt][g][p], d, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t w = dm[r * kNb + g];
-            float x = s[nt][half * 4 + r];
-            x = fmaf(half_bits(w & 0xFFFFu), d[r], x);
-            s[nt][half * 4 + r] = fmaf(half_bits(w >> 16), qsum[nt][g], x);
-          }
-        }
-      }
+        for (int r = 0; r < 4; ++r) s[nt][half * 4 + r] = acc[nt][r];
     }
 
-    float p[NT][8];
+    h8v p[NT][kPp];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top = kNegInf;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float x = s[nt][k] * c2;
         if (!full) {
           const int tok = pos + (k >> 2) * 16 + quad * 4 + (k & 3);
           const bool seen = tok <= pos_of[nt] && (win == 0 || pos_of[nt] - tok < win || tok < sinks);
-          x = seen ? x : kNegInf;
+          s[nt][k] = seen ? s[nt][k] : kNegInf;
         }
-        s[nt][k] = x;
-        top = fmaxf(top, x);
+        s[nt][k] *= cs[nt];  // rounded before the subtraction: the largest score's weight is a power of 2
+        top = fmaxf(top, s[nt][k]);
       }
-      if (__any(top > m[nt] + kSlack)) {
+      if (__any(top > m[nt] + kRaise)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float up = fmaxf(m[nt], top);
         const float f = m[nt] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[nt] - up);
         m[nt] = up;
         l[nt] *= f;
+        lin[nt] *= f;
 #pragma unroll
         for (int n = 0; n < DIM / 16; ++n) o[nt][n] *= f;
-#pragma unroll
-        for (int g = 0; g < kNb; ++g) msum[nt][g] *= f;
       }
-      const float ref = m[nt] == kNegInf ? 0.0f : m[nt];
+      const float ref = m[nt] == kNegInf ? 0.0f : m[nt] - kBias;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        p[nt][k] = __builtin_amdgcn_exp2f(s[nt][k] - ref);
-        l[nt] += p[nt][k];
+        float x = __builtin_amdgcn_exp2f(s[nt][k] - ref);
+        l[nt] += x;
+#pragma unroll
+        for (int z = 0; z < kPp; ++z) {
+          p[nt][z][k] = (_Float16)x;
+          x -= (float)p[nt][z][k];
+        }
       }
     }
 
-    const uint4* vd = reinterpret_cast<const uint4*>(sc + 32 * kNb);
+    if constexpr (kExact) {
+      const h8v w = __builtin_bit_cast(h8v, t.vs);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int z = kPp - 1; z >= 0; --z) lin[nt] = mfma(w, p[nt][z], lin[nt]);
+    }
 #pragma unroll
     for (int g = 0; g < kNb; ++g) {
-      const uint4 dw = vd[g * 4 + quad], mw = vd[(kNb + g) * 4 + quad];
-      const uint32_t dws[4] = {dw.x, dw.y, dw.z, dw.w}, mws[4] = {mw.x, mw.y, mw.z, mw.w};
-      const bf8v va = codes8(cur.vc[2 * g]), vb = codes8(cur.vc[2 * g + 1]);
+      const uint4 dw = sc[g * 4 + quad];
+      const uint32_t d[4] = {dw.x, dw.y, dw.z, dw.w};
+      if constexpr (kExact) {
+        h2v dh[4], dl[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pd[8];
+        for (int z = 0; z < 4; ++z) split_step(d[z], dh[z], dl[z]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t sel = k & 1 ? dws[k >> 1] >> 16 : dws[k >> 1] & 0xFFFFu;
-          const uint32_t sem = k & 1 ? mws[k >> 1] >> 16 : mws[k >> 1] & 0xFFFFu;
-          pd[k] = p[nt][k] * half_bits(sel);
-          msum[nt][g] = fmaf(p[nt][k], half_bits(sem), msum[nt][g]);
+        for (int half = 0; half < 2; ++half) {
+          const int n = 2 * g + half;
+          h2v c[4], x[4];
+          codes8(t.vc[n], c);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[z] = __builtin_elementwise_fma(c[z], dl[z], -times8(dl[z]));
+          const h8v lo = join8(x);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[z] = __builtin_elementwise_fma(c[z], dh[z], -times8(dh[z]));
+          const h8v hi = join8(x);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            f4v acc = o[nt][n];
+            acc = mfma(lo, p[nt][1], acc);
+            acc = mfma(lo, p[nt][0], acc);
+            acc = mfma(hi, p[nt][1], acc);
+            o[nt][n] = mfma(hi, p[nt][0], acc);
+          }
         }
-        bf8v part[kPp];
-        split8<kPp>(pd, part);
+      } else {
+        const uint4 mw = sc[(kNb + g) * 4 + quad];
+        const uint32_t mm[4] = {mw.x, mw.y, mw.z, mw.w};
 #pragma unroll
-        for (int x = kPp - 1; x >= 0; --x) {
-          o[nt][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, part[x], o[nt][2 * g], 0, 0, 0);
-          o[nt][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, part[x], o[nt][2 * g + 1], 0, 0, 0);
+        for (int half = 0; half < 2; ++half) {
+          const int n = 2 * g + half;
+          h2v c[4];
+          codes8(t.vc[n], c);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) c[z] = __builtin_elementwise_fma(c[z], as_h2(d[z]), as_h2(mm[z]));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) o[nt][n] = mfma(join8(c), p[nt][0], o[nt][n]);
         }
       }
     }
+  };
+  for (; v < v1; v += kWaves) {
+    step(ta, tb);
+    v += kWaves;
+    if (v >= v1) break;
+    step(tb, ta);
   }
 
   // Join the four waves, 16 rows at a time.
@@ -330,13 +377,10 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
     ls += __shfl_xor(ls, 32);
     if (nt > 0) __syncthreads();
 #pragma unroll
-    for (int g = 0; g < kNb; ++g) {
-      float x = msum[nt][g];
-      x += __shfl_xor(x, 16);
-      x += __shfl_xor(x, 32);
+    for (int n = 0; n < DIM / 16; ++n) *reinterpret_cast<f4v*>(&obuf[wave][col][n * 16 + quad * 4]) = o[nt][n];
+    if constexpr (kExact) {
 #pragma unroll
-      for (int z = 0; z < 2; ++z)
-        *reinterpret_cast<f4v*>(&obuf[wave][col][(2 * g + z) * 16 + quad * 4]) = o[nt][2 * g + z] + x;
+      for (int r = 0; r < 4; ++r) linear[wave][col][quad * 4 + r] = lin[nt][r];
     }
     if (quad == 0) ml[wave][col][0] = m[nt], ml[wave][col][1] = ls;
     __syncthreads();
@@ -353,10 +397,15 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
       }
       const int j = r / a.group, hq = h * a.group + r - j * a.group;
       const int64_t row = ((int64_t)i * a.rows.q_len + j) * a.heads + hq;
-      float x[DIM / 16];
+      float x[DIM / 16], same = 0.0f;
+      if constexpr (kExact) {
+        const int g = ch0 / 32;  // a thread's channels are of one block
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) same = fmaf(f[w], fmaf(8.0f, linear[w][oc][g], linear[w][oc][kNb + g]), same);
+      }
 #pragma unroll
       for (int k = 0; k < DIM / 16; ++k) {
-        x[k] = 0.0f;
+        x[k] = same;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) x[k] = fmaf(f[w], obuf[w][oc][ch0 + k], x[k]);
       }
@@ -365,11 +414,13 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
         const int pos = e.len - e.c + j;
         const bool none = r >= e.c * a.group || pos < sp.first || pos > sp.last || top == kNegInf;
 #pragma unroll
-        for (int k = 0; k < DIM / 16; ++k) store_elem<T>(a.out, at + k, none ? 0.0f : x[k] / total);
+        for (int k = 0; k < DIM / 16; ++k) x[k] = none ? 0.0f : x[k] / total;
+#pragma unroll
+        for (int k = 0; k < DIM / 16; k += 4) store4<T>(a.out, at + k, a.ovec, {x[k], x[k + 1], x[k + 2], x[k + 3]});
       } else {
         float* dst = a.ws + (row * splits + split) * DIM + ch0;
 #pragma unroll
-        for (int k = 0; k < DIM / 16; ++k) dst[k] = x[k];
+        for (int k = 0; k < DIM / 16; k += 4) *reinterpret_cast<f4v*>(dst + k) = f4v{x[k], x[k + 1], x[k + 2], x[k + 3]};
         if ((tid & 15) == 0) {
           float* st = a.ws + part_floats + (row * splits + split) * 2;
           st[0] = top, st[1] = total;
@@ -379,63 +430,98 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
   }
 }
 
-// Joins the splits: one wave per query row.
+// Joins the splits of one query row per workgroup: the factors first, then
+// every thread adds four channels of every kParts-th split.
 template <int DIM, int T>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(KvAttend a, int cols, int chunk, int splits,
                                                                int64_t part_floats) {
-  const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= (int64_t)a.rows.n * a.rows.q_len * a.heads) return;
+  constexpr int kParts = kThreads / (DIM / 4);
+  __shared__ float factor[kMaxSplits];
+  __shared__ float red[2][kWaves];
+  __shared__ f4v sums[kParts][DIM / 4];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
   const int hq = (int)(row % a.heads);
   const int64_t ij = row / a.heads;
   const int j = (int)(ij % a.rows.q_len), i = (int)(ij / a.rows.q_len);
   const Entry e = load_entry(a.kv, a.rows, i);
   const int r = j * a.group + hq % a.group;
-  const Span sp = block_span(a, e, r / cols * cols, cols);
+  const Span sp = row_span(e, r / cols * cols, cols, a.group, (int)a.max_len, (int)a.window, (int)a.sinks);
   const int pos = e.len - e.c + j;
   const int used = j < e.c && pos >= sp.first && pos <= sp.last ? (sp.tiles + chunk - 1) / chunk : 0;
   const float* st = a.ws + part_floats + row * splits * 2;
-  const float* src = a.ws + row * splits * DIM + lane * (DIM / 64);
-  float top = kNegInf, total = 0.0f;
-  for (int s = 0; s < used; ++s) top = fmaxf(top, st[2 * s]);
-  float x[DIM / 64];
+  float top = kNegInf;
+  for (int s = tid; s < used; s += kThreads) top = fmaxf(top, st[2 * s]);
 #pragma unroll
-  for (int k = 0; k < DIM / 64; ++k) x[k] = 0.0f;
-  for (int s = 0; s < used; ++s) {
+  for (int z = 32; z >= 1; z >>= 1) top = fmaxf(top, __shfl_xor(top, z));
+  if ((tid & 63) == 0) red[0][tid >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red[0][w]);
+  float total = 0.0f;
+  for (int s = tid; s < used; s += kThreads) {
     const float f = st[2 * s] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(st[2 * s] - top);
+    factor[s] = f;
     total = fmaf(f, st[2 * s + 1], total);
-#pragma unroll
-    for (int k = 0; k < DIM / 64; ++k) x[k] = fmaf(f, src[(int64_t)s * DIM + k], x[k]);
   }
-  const int64_t at = (int64_t)i * a.os[0] + (int64_t)j * a.os[1] + (int64_t)hq * a.os[2] + lane * (DIM / 64);
 #pragma unroll
-  for (int k = 0; k < DIM / 64; ++k) store_elem<T>(a.out, at + k, top == kNegInf ? 0.0f : x[k] / total);
+  for (int z = 32; z >= 1; z >>= 1) total += __shfl_xor(total, z);
+  if ((tid & 63) == 0) red[1][tid >> 6] = total;
+  __syncthreads();
+  const int c4 = tid % (DIM / 4), part = tid / (DIM / 4);
+  const f4v* src = reinterpret_cast<const f4v*>(a.ws + row * splits * DIM) + c4;
+  f4v x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = part; s < used; s += kParts) {
+    const f4v y = src[(int64_t)s * (DIM / 4)];
+    const float f = factor[s];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = fmaf(f, y[k], x[k]);
+  }
+  sums[part][c4] = x;
+  __syncthreads();
+  if (tid >= DIM / 4) return;
+  total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) total += red[1][w];
+#pragma unroll
+  for (int z = 1; z < kParts; ++z) x += sums[z][tid];
+  const bool none = top == kNegInf;
+  float y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = none ? 0.0f : x[k] / total;
+  const int64_t at = (int64_t)i * a.os[0] + (int64_t)j * a.os[1] + (int64_t)hq * a.os[2] + tid * 4;
+  store4<T>(a.out, at, a.ovec, y);
 }
 
-int64_t part_floats_of(const KvAttend& a, int splits) {
-  return (int64_t)a.rows.n * a.rows.q_len * a.heads * splits * a.kv.head_dim;
+template <int DIM, int T>
+hipError_t launch_join(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
+  const int64_t rows = (int64_t)a.rows.n * a.rows.q_len * a.heads;
+  QBL_LAUNCH((attend_join_kernel<DIM, T>), dim3((unsigned)rows), dim3(kThreads), 0, lc, a, p.cols, p.chunk, p.splits,
+             attend_part_floats(a, p));
+  return hipGetLastError();
 }
 
 template <int DIM, int T, int NT>
-hipError_t launch_nt(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
+hipError_t launch_few(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
   const int sh = __builtin_ctz((unsigned)a.kv.page_tokens);
   const int64_t grid = (int64_t)a.rows.n * a.kv.n_kv_heads * p.row_blocks * p.splits;
-  const int64_t pf = part_floats_of(a, p.splits);
   QBL_LAUNCH((attend_kernel<DIM, T, NT>), dim3((unsigned)grid), dim3(kThreads), 0, lc, a, p.row_blocks, p.chunk, p.splits,
-             sh, pf);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t rows = (int64_t)a.rows.n * a.rows.q_len * a.heads;
-  QBL_LAUNCH((attend_join_kernel<DIM, T>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, lc, a, p.cols,
-             p.chunk, p.splits, pf);
+             sh, attend_part_floats(a, p));
   return hipGetLastError();
 }
 
 template <int DIM, int T>
 hipError_t launch_type(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
-  if constexpr (DIM <= 128)
-    if (p.cols == 32) return launch_nt<DIM, T, 2>(a, p, lc);
-  return launch_nt<DIM, T, 1>(a, p, lc);
+  hipError_t e;
+  if (p.many) {
+    e = launch_attend_rows(a, p, lc);
+  } else if (DIM <= 128 && p.cols == 32) {
+    if constexpr (DIM <= 128) e = launch_few<DIM, T, 2>(a, p, lc);
+  } else {
+    e = launch_few<DIM, T, 1>(a, p, lc);
+  }
+  return e != hipSuccess || p.splits == 1 ? e : launch_join<DIM, T>(a, p, lc);
 }
 
 template <int DIM>
@@ -453,9 +539,10 @@ hipError_t launch_dim(const KvAttend& a, const AttendPlan& p, const LaunchCtx& l
 AttendPlan attend_plan(const KvAttend& a) {
   AttendPlan p;
   const int64_t rows = (int64_t)a.rows.q_len * a.group;
+  p.many = a.dtype == QBL_T_BF16 && rows > 32;
   // Two row blocks per workgroup read the cache once for both; 256 channels
   // leave registers for one only (two spill).
-  p.cols = rows <= 16 || a.kv.head_dim == 256 ? 16 : 32;
+  p.cols = p.many ? kManyRows : rows <= 16 || a.kv.head_dim == 256 ? 16 : 32;
   p.row_blocks = (int)((rows + p.cols - 1) / p.cols);
   // Tiles that a block of rows can see at most.
   const int64_t len = std::min<int64_t>(a.max_len, (int64_t)a.kv.max_pages * a.kv.page_tokens);
@@ -465,9 +552,15 @@ AttendPlan attend_plan(const KvAttend& a) {
     tiles = std::min<int64_t>(tiles, (span + 62) / 32 + (std::min<int64_t>(a.sinks, len) + 31) / 32);
   }
   tiles = std::max<int64_t>(tiles, 1);
-  // Enough workgroups to fill the device twice over, each wave at least one tile.
   const int64_t base = (int64_t)a.rows.n * a.kv.n_kv_heads * p.row_blocks;
-  const int64_t want = std::min<int64_t>(std::max<int64_t>(1, 1024 / base), (tiles + kWaves - 1) / kWaves);
+  int64_t want;
+  if (p.many) {
+    // Two workgroups per CU, each at least 8 tiles.
+    want = std::min<int64_t>(std::max<int64_t>(1, 512 / base), (tiles + 7) / 8);
+  } else {
+    // Enough workgroups to fill the device twice over, each wave at least one tile.
+    want = std::min<int64_t>(std::max<int64_t>(1, 1024 / base), (tiles + kWaves - 1) / kWaves);
+  }
   p.chunk = (int)((tiles + want - 1) / want);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
   const int64_t out_rows = (int64_t)a.rows.n * a.rows.q_len * a.heads;

@@ -1,0 +1,97 @@
+// Device helpers shared by the attention kernels over the 4-bit cache (gfx950,
+// wave64).  Internal.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "qbl_cache_device.h"
+
+namespace qbl {
+namespace {
+
+typedef _Float16 h2v __attribute__((ext_vector_type(2)));
+typedef _Float16 h4v __attribute__((ext_vector_type(4)));
+typedef _Float16 h8v __attribute__((ext_vector_type(8)));
+typedef float f4v __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLog2e = 1.44269504088896340736f;
+// Softmax weights are 2^kBias times exp(score - reference), and the reference
+// is raised when a score passes it by kRaise (exponents of 2): weights stay
+// below 2^15, and f16 holds those from 2^-25 on with all of its bits.
+constexpr float kBias = 11.0f, kRaise = 4.0f;
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Exponent that brings a row's largest magnitude into [2^top, 2^(top+1)) (less
+// where all of the row is tiny; 0 for a row of zeros or one that is not
+// finite).  `big` is this lane's part; lanes l, l^16 and l^32 share a row.
+__device__ __forceinline__ int row_exponent(float big, int top) {
+  big = fmaxf(big, __shfl_xor(big, 16));
+  big = fmaxf(big, __shfl_xor(big, 32));
+  return big > 0.0f && big < __builtin_inff() ? min(top + 127 - (int)(__float_as_uint(big) >> 23), 100) : 0;
+}
+
+// Halves of x (tokens 4 quad + 0..3 and 16 + 4 quad + 0..3 of the tile at pos)
+// whose token no row of the span sees become 0.
+__device__ __forceinline__ uint4 hide(uint4 x, int pos, int quad, const Span& sp, int win, int sinks) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int tok = pos + (k >> 2) * 16 + quad * 4 + (k & 3);
+    const bool seen = tok <= sp.last && (win == 0 || tok < sinks || tok > sp.first - win);
+    if (!seen) w[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Codes of one word as f16, in the order channel (or token) 0..7.  A nibble n
+// read as an e4m3 number is n * 2^-9 exactly (subnormal up to 7, then the first
+// binade), and the conversion multiplies by 2^9.
+__device__ __forceinline__ void codes8(uint32_t w, h2v (&c)[4]) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  c[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false);
+  c[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true);
+  c[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false);
+  c[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true);
+}
+
+__device__ __forceinline__ h8v join8(const h2v (&c)[4]) {
+  return h8v{c[0][0], c[0][1], c[1][0], c[1][1], c[2][0], c[2][1], c[3][0], c[3][1]};
+}
+
+__device__ __forceinline__ h2v as_h2(uint32_t w) { return __builtin_bit_cast(h2v, w); }
+
+// Both halves of a word set to its low (high) half.
+__device__ __forceinline__ h2v low2(uint32_t w) { return as_h2(__builtin_amdgcn_perm(w, w, 0x01000100u)); }
+__device__ __forceinline__ h2v high2(uint32_t w) { return as_h2(__builtin_amdgcn_perm(w, w, 0x03020302u)); }
+
+// Page of a slot's position through the scalar cache (the table is not written
+// by the kernels that use this): uniform arguments give a scalar load.
+__device__ __forceinline__ int page_of_uniform(const qbl_kv& kv, int slot, int pos, int page_shift) {
+  typedef const __attribute__((address_space(4))) int32_t* cptr;
+  const int p = ((cptr)(uintptr_t)(kv.table + (int64_t)slot * kv.max_pages))[pos >> page_shift];
+  return p >= 0 && p < kv.n_pages ? p : -1;
+}
+
+// Which (entry, head) pair and which of its `per` workgroups workgroup b is.
+// The 8 XCDs take workgroups in turn; pair p goes to XCD p % 8, so that the
+// workgroups that read the same part of the cache share an L2.  Pairs past the
+// last multiple of 8 are spread over all XCDs.
+__device__ __forceinline__ void xcd_pair(int b, int pairs, int per, int& pair, int& part) {
+  const int even = pairs & ~7;
+  if (b < even * per) {
+    const int k = b >> 3;
+    pair = (k / per) * 8 + (b & 7);
+    part = k % per;
+  } else {
+    const int r = b - even * per, left = pairs - even;
+    pair = even + r % left;
+    part = r / left;
+  }
+}
+
+}  // namespace
+}  // namespace qbl

@@ -1,0 +1,325 @@
+// Attention over the paged 4-bit cache for many query rows (prompts), bf16.
+//
+//   out = softmax(c q K^T) V,  K and V in blocks of 32 channels: x = d*code + m.
+//
+// A workgroup serves 128 query rows (new tokens times the query heads that
+// share a key/value head), 32 per wave, against a run of tiles.  Each step's
+// tiles are dequantised once for all four waves: a thread turns 16 bytes of
+// codes into 32 values with one packed f16 multiply-add per two (single
+// rounding, 2^-12 relative, against bf16 outputs' 2^-9) and stores them in LDS
+// in the order of the matrix instructions' operands, 16 bytes per lane, so
+// that neither side conflicts on banks.  The query rows are scaled by a power
+// of two per row so that bf16's range fits f16 (exact above 2^-28 of the row's
+// largest value).
+//
+// Scores are computed transposed (tokens are the rows of the product), so a
+// lane holds 16 tokens' scores of one query row, exactly the operand of the
+// second product: no data moves between lanes.  One-pass softmax: the
+// reference maximum is raised, and the sums rescaled, only when a score passes
+// it by 4 in the exponent of 2.  Weights carry a factor 2^11, so that they use
+// f16's range from 2^-25 of the reference on at full precision.
+//
+// Two buffers in LDS: while one is multiplied, the next step is dequantised
+// into the other and the loads of the one after are in flight; one barrier per
+// step.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "qbl_attend_device.h"
+
+namespace qbl {
+namespace {
+
+constexpr int kRowWaves = kManyRows / 32;
+constexpr int kRowThreads = 64 * kRowWaves;
+constexpr int kFar = 1 << 30;  // position of a tile that nobody sees
+
+template <int DIM>
+struct RowTiles {
+  static constexpr int kNb = DIM / 32;
+  static constexpr int kTiles = DIM == 256 ? 1 : 2;              // per step
+  static constexpr int kItems = kTiles * 2 * DIM / kRowThreads;  // 16-byte pieces of codes per thread and step
+  static constexpr int kHalves = 32 * DIM;                       // of one tile's keys (or values) in LDS
+  uint4 code[kItems];
+  uint4 scale[kItems][4];  // keys: [0]; values: d and m of two channel blocks
+  int pos[kItems];         // the piece's tile
+};
+
+template <int DIM>
+__device__ __forceinline__ void load_step(const KvAttend& a, const Entry& e, const Span& sp, int h, int v, int v1,
+                                          int page_shift, int tid, RowTiles<DIM>& t) {
+  using R = RowTiles<DIM>;
+  constexpr int kNb = R::kNb;
+#pragma unroll
+  for (int i = 0; i < R::kItems; ++i) {
+    const int id = tid + i * kRowThreads;
+    const int part = __builtin_amdgcn_readfirstlane(id / DIM);  // tile * 2 + (values)
+    const int vt = v + (part >> 1);
+    t.pos[i] = kFar;
+    t.code[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t.scale[i][k] = make_uint4(0, 0, 0, 0);
+    if (vt >= v1) continue;
+    const int pos = span_pos(sp, vt);
+    const int page = page_of_uniform(a.kv, e.slot, pos, page_shift);
+    if (page < 0) continue;
+    t.pos[i] = pos;
+    const uint8_t* p = tile_ptr<DIM>(a.kv, a.layer, page, h, pos, page_shift);
+    const int x = id % DIM;
+    if (!(part & 1)) {
+      const uint4* kc = reinterpret_cast<const uint4*>(p);
+      const uint8_t* ks = p + 16 * DIM;
+      const int tok = x & 31, q = x >> 5;
+      if constexpr (DIM == 64) {
+        t.code[i] = kc[tok * 2 + q];
+        const uint2 s = *reinterpret_cast<const uint2*>(ks + tok * 8);
+        t.scale[i][0] = make_uint4(s.x, s.y, s.x, s.y);
+      } else {
+        t.code[i] = kc[((q >> 2) * 32 + tok) * 4 + (q & 3)];
+        t.scale[i][0] = *reinterpret_cast<const uint4*>(ks + (tok * kNb + (q >> 2) * 4) * 4);
+      }
+    } else {
+      const uint4* vc = reinterpret_cast<const uint4*>(p + 16 * DIM + 128 * kNb);
+      const uint4* vs = reinterpret_cast<const uint4*>(p + 32 * DIM + 128 * kNb);
+      const int ln = x & 15, quad = x >> 4 & 3, c = x >> 6;
+      t.code[i] = vc[(c * 16 + ln) * 4 + quad];
+      t.scale[i][0] = vs[(2 * c) * 4 + quad];
+      t.scale[i][1] = vs[(2 * c + 1) * 4 + quad];
+      t.scale[i][2] = vs[(kNb + 2 * c) * 4 + quad];
+      t.scale[i][3] = vs[(kNb + 2 * c + 1) * 4 + quad];
+    }
+  }
+}
+
+__device__ __forceinline__ bool all_seen(int pos, int first, int last, int win, int sinks) {
+  return pos + 31 <= first && (win == 0 || pos > last - win || pos + 31 < sinks);
+}
+
+template <int DIM>
+__device__ __forceinline__ void store_step(RowTiles<DIM>& t, const Span& sp, int win, int sinks, int tid, h8v* lds) {
+  using R = RowTiles<DIM>;
+#pragma unroll
+  for (int i = 0; i < R::kItems; ++i) {
+    const int id = tid + i * kRowThreads;
+    const int part = __builtin_amdgcn_readfirstlane(id / DIM);
+    const int x = id % DIM;
+    h8v* dst = lds + part * (R::kHalves / 8);
+    const uint32_t w[4] = {t.code[i].x, t.code[i].y, t.code[i].z, t.code[i].w};
+    if (!(part & 1)) {
+      const int tok = x & 31, q = x >> 5;
+      const uint32_t s[4] = {t.scale[i][0].x, t.scale[i][0].y, t.scale[i][0].z, t.scale[i][0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h2v c[4];
+        codes8(w[k], c);
+        const h2v d = low2(s[k]), m = high2(s[k]);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) c[z] = __builtin_elementwise_fma(c[z], d, m);
+        // eighth of the channels: 4 * block + quad
+        const int f = DIM == 64 ? 4 * (k & 1) + 2 * q + (k >> 1) : 4 * ((q >> 2) * 4 + k) + (q & 3);
+        dst[f * 32 + tok] = join8(c);
+      }
+    } else {
+      const int ln = x & 15, quad = x >> 4 & 3, c64 = x >> 6;
+      if (t.pos[i] != kFar && !all_seen(t.pos[i], sp.first, sp.last, win, sinks)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t.scale[i][k] = hide(t.scale[i][k], t.pos[i], quad, sp, win, sinks);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h2v c[4];
+        codes8(w[k], c);
+        const uint4 d = t.scale[i][k >> 1], m = t.scale[i][2 + (k >> 1)];
+        c[0] = __builtin_elementwise_fma(c[0], as_h2(d.x), as_h2(m.x));
+        c[1] = __builtin_elementwise_fma(c[1], as_h2(d.y), as_h2(m.y));
+        c[2] = __builtin_elementwise_fma(c[2], as_h2(d.z), as_h2(m.z));
+        c[3] = __builtin_elementwise_fma(c[3], as_h2(d.w), as_h2(m.w));
+        dst[((2 * c64 + (k >> 1)) * 4 + quad) * 32 + 16 * (k & 1) + ln] = join8(c);
+      }
+    }
+  }
+}
+
+template <int DIM, int T>
+__global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_kernel(KvAttend a, int row_blocks, int chunk, int splits,
+                                                                     int page_shift, int64_t part_floats) {
+  using R = RowTiles<DIM>;
+  constexpr int kTiles = R::kTiles, kBuf = kTiles * 2 * R::kHalves / 8;
+  __shared__ h8v lds[2][kBuf];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int col = lane & 31, hf = lane >> 5;
+  int pair, part;
+  xcd_pair(blockIdx.x, a.rows.n * a.kv.n_kv_heads, row_blocks * splits, pair, part);
+  // the rows that see most first: they take longest
+  const int rb = row_blocks - 1 - part / splits, split = part % splits;
+  const int h = pair % a.kv.n_kv_heads, i = pair / a.kv.n_kv_heads;
+  const Entry e = load_entry(a.kv, a.rows, i);
+  const int r0 = rb * kManyRows;
+  const int win = (int)a.window, sinks = (int)a.sinks;
+  const Span sp = row_span(e, r0, kManyRows, a.group, (int)a.max_len, win, sinks);
+  if (splits > 1 && split * chunk >= sp.tiles) return;
+  const int v0 = split * chunk, v1 = min(sp.tiles, v0 + chunk);
+
+  RowTiles<DIM> t;
+  if (v0 < v1) load_step<DIM>(a, e, sp, h, v0, v1, page_shift, tid, t);
+
+  // This lane's row and its queries, times a power of two.
+  const int r = r0 + wave * 32 + col;
+  const int j = r / a.group, hq = h * a.group + r - j * a.group;
+  const int pos_j = e.len - e.c + j;
+  const bool ok = r < e.c * a.group && pos_j >= sp.first && pos_j <= sp.last;
+  const int pos_of = ok ? pos_j : -1;
+  const int64_t row_at = (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] + (int64_t)hq * a.qs[2];
+  h8v q[DIM / 16];
+  float cs;
+  {
+    float x[DIM / 16][8], big = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < DIM / 16; ++ks) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[ks][k] = 0.0f;
+      if (ok) load8<T>(a.q, row_at + ks * 16 + hf * 8, a.vec, x[ks]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[ks][k]));
+    }
+    big = fmaxf(big, __shfl_xor(big, 32));
+    const int ex = big > 0.0f && big < __builtin_inff() ? min(14 + 127 - (int)(__float_as_uint(big) >> 23), 100) : 0;
+    const float sign = a.scale < 0.0f ? -pow2(ex) : pow2(ex);
+#pragma unroll
+    for (int ks = 0; ks < DIM / 16; ++ks)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[ks][k] = (_Float16)(x[ks][k] * sign);
+    cs = fabsf(a.scale) * kLog2e * pow2(-ex);
+  }
+
+  f16v o[DIM / 32];
+#pragma unroll
+  for (int c = 0; c < DIM / 32; ++c)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[c][k] = 0.0f;
+  float m = kNegInf, l = 0.0f;
+
+  if (v0 < v1) {
+    store_step<DIM>(t, sp, win, sinks, tid, lds[0]);
+    load_step<DIM>(a, e, sp, h, v0 + kTiles, v1, page_shift, tid, t);
+  }
+  __syncthreads();
+
+  int buf = 0;
+  for (int v = v0; v < v1; v += kTiles, buf ^= 1) {
+    f16v s[kTiles];
+#pragma unroll
+    for (int z = 0; z < kTiles; ++z) {
+      const h8v* kt = lds[buf] + (2 * z) * (R::kHalves / 8) + lane;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s[z][k] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < DIM / 16; ++ks) s[z] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kt[ks * 64], q[ks], s[z], 0, 0, 0);
+    }
+    if (v + kTiles < v1) {
+      store_step<DIM>(t, sp, win, sinks, tid, lds[buf ^ 1]);
+      load_step<DIM>(a, e, sp, h, v + 2 * kTiles, v1, page_shift, tid, t);
+    }
+    float top = kNegInf;
+#pragma unroll
+    for (int z = 0; z < kTiles; ++z) {
+      int pos = kFar;
+      if (v + z < v1) {
+        pos = span_pos(sp, v + z);
+        if (page_of_uniform(a.kv, e.slot, pos, page_shift) < 0) pos = kFar;
+      }
+      if (!all_seen(pos, sp.first, sp.last, win, sinks)) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int tok = pos + (k >> 2) * 8 + hf * 4 + (k & 3);
+          const bool seen = tok <= pos_of && (win == 0 || pos_of - tok < win || tok < sinks);
+          s[z][k] = seen ? s[z][k] : kNegInf;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, s[z][k]);
+    }
+    top *= cs;
+    if (__any(top > m + kRaise)) {
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float up = fmaxf(m, top);
+      const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - up);
+      m = up;
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < DIM / 32; ++c) o[c] *= f;
+    }
+    const float ref = m == kNegInf ? 0.0f : m - kBias;
+#pragma unroll
+    for (int z = 0; z < kTiles; ++z) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        s[z][k] = __builtin_amdgcn_exp2f(fmaf(s[z][k], cs, -ref));
+        l += s[z][k];
+      }
+      const h8v* vt = lds[buf] + (2 * z + 1) * (R::kHalves / 8) + lane;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        h8v p;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = (_Float16)s[z][(k >> 2) * 8 + w * 4 + (k & 3)];
+#pragma unroll
+        for (int c = 0; c < DIM / 32; ++c) o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vt[(c * 2 + w) * 64], p, o[c], 0, 0, 0);
+      }
+    }
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32);
+  if (r >= a.rows.q_len * a.group) return;
+  if (splits == 1) {
+    const bool none = !ok || m == kNegInf;
+    const float inv = none ? 0.0f : 1.0f / l;
+    const int64_t at = (int64_t)i * a.os[0] + (int64_t)j * a.os[1] + (int64_t)hq * a.os[2] + hf * 4;
+#pragma unroll
+    for (int c = 0; c < DIM / 32; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) x[z] = none ? 0.0f : o[c][4 * k + z] * inv;
+        store4<T>(a.out, at + c * 32 + k * 8, a.ovec, x);
+      }
+  } else {
+    const int64_t row = ((int64_t)i * a.rows.q_len + j) * a.heads + hq;
+    float* dst = a.ws + (row * splits + split) * DIM + hf * 4;
+#pragma unroll
+    for (int c = 0; c < DIM / 32; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<f4v*>(dst + c * 32 + k * 8) =
+            f4v{o[c][4 * k], o[c][4 * k + 1], o[c][4 * k + 2], o[c][4 * k + 3]};
+    if (hf == 0) {
+      float* st = a.ws + part_floats + (row * splits + split) * 2;
+      st[0] = m, st[1] = l;
+    }
+  }
+}
+
+template <int DIM>
+hipError_t launch_dim(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
+  const int sh = __builtin_ctz((unsigned)a.kv.page_tokens);
+  const int64_t grid = (int64_t)a.rows.n * a.kv.n_kv_heads * p.row_blocks * p.splits;
+  QBL_LAUNCH((attend_rows_kernel<DIM, QBL_T_BF16>), dim3((unsigned)grid), dim3(kRowThreads), 0, lc, a, p.row_blocks,
+             p.chunk, p.splits, sh, attend_part_floats(a, p));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attend_rows(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
+  switch (a.kv.head_dim) {
+    case 64: return launch_dim<64>(a, p, lc);
+    case 128: return launch_dim<128>(a, p, lc);
+    case 256: return launch_dim<256>(a, p, lc);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace qbl

@@ -308,6 +308,7 @@ extern "C" qbl_status qbl_kv_attend(const qbl_kv* kv, int32_t layer, const int32
     a.out = out;
     for (int i = 0; i < 3; ++i) a.qs[i] = q_strides[i], a.os[i] = out_strides[i];
     a.vec = rows_vectorise(q, q_strides, dtype);
+    a.ovec = rows_vectorise(out, out_strides, dtype);
     a.scale = scale == 0.0f ? 1.0f / std::sqrt((float)kv->head_dim) : scale;
     a.ws = static_cast<float*>(ws);
     return done(qbl::launch_kv_attend(a, p, on(stream)), "attend launch");

@@ -63,5 +63,26 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
   if constexpr (T == QBL_T_BF16) static_cast<__hip_bfloat16*>(p)[i] = __float2bfloat16(v);
 }
 
+// Four consecutive elements from i; vec: p + i is aligned to all four.
+template <int T>
+__device__ __forceinline__ void store4(void* p, int64_t i, bool vec, const float (&x)[4]) {
+  if (!vec) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store_elem<T>(p, i + k, x[k]);
+    return;
+  }
+  if constexpr (T == QBL_T_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (T == QBL_T_F16) w[k] = __half_as_ushort(__float2half_rn(x[k]));
+      else w[k] = __builtin_bit_cast(unsigned short, (__bf16)x[k]);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
+}
+
 }  // namespace
 }  // namespace qbl

@@ -54,13 +54,16 @@ struct KvAttend {
   int64_t qs[3], os[3];
   int dtype;
   int vec;               // 1: every row of q is 16-byte aligned
+  int ovec;              // 1: every row of out is
   int64_t max_len, window, sinks;
   float scale;
   float* ws;             // partial results of the splits (attend_plan)
 };
 // How a call is split: rows of one key/value head per workgroup and tiles of
 // the cache per split.
+constexpr int kManyRows = 128;  // query rows per workgroup of the kernel for many rows
 struct AttendPlan {
+  bool many;         // the kernel for many rows
   int cols;          // query rows per workgroup
   int row_blocks;    // workgroups along the rows
   int chunk;         // tiles per split
@@ -68,6 +71,11 @@ struct AttendPlan {
   int64_t ws_bytes;
 };
 AttendPlan attend_plan(const KvAttend& a);
+// Floats of partial sums in the workspace, before the splits' maxima and weights.
+inline int64_t attend_part_floats(const KvAttend& a, const AttendPlan& p) {
+  return (int64_t)a.rows.n * a.rows.q_len * a.heads * p.splits * a.kv.head_dim;
+}
+hipError_t launch_attend_rows(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc);
 hipError_t launch_kv_attend(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc);
 
 struct VerifyArgs {
