@@ -221,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
     const bool full = pos + 31 <= sp.first && (win == 0 || pos >= sp.last - win + 1 || pos + 31 < sinks);
     // Value scales of tokens that no row sees become 0, so that whatever is
     // stored there meets a weight of 0 as a finite number.
-    if (!full) t.vs = hide(t.vs, pos, quad, sp, win, sinks);
+    if (!full) t.vs = and4(t.vs, seen_mask(pos, quad, sp.last, win == 0 ? -1 : sp.first - win, sinks));
     wave_sync();
     if (col < 2 * kNb) sc[col * 4 + quad] = t.vs;
     wave_sync();

@@ -34,18 +34,20 @@ __device__ __forceinline__ int row_exponent(float big, int top) {
   return big > 0.0f && big < __builtin_inff() ? min(top + 127 - (int)(__float_as_uint(big) >> 23), 100) : 0;
 }
 
-// Halves of x (tokens 4 quad + 0..3 and 16 + 4 quad + 0..3 of the tile at pos)
-// whose token no row of the span sees become 0.
-__device__ __forceinline__ uint4 hide(uint4 x, int pos, int quad, const Span& sp, int win, int sinks) {
-  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// Which halves of a row of value scales (tokens 4 quad + 0..3 and 16 + 4 quad +
+// 0..3 of the tile at pos) belong to tokens with t <= hi and (t > lo or t < sinks).
+__device__ __forceinline__ uint4 seen_mask(int pos, int quad, int hi, int lo, int sinks) {
+  uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int tok = pos + (k >> 2) * 16 + quad * 4 + (k & 3);
-    const bool seen = tok <= sp.last && (win == 0 || tok < sinks || tok > sp.first - win);
-    if (!seen) w[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  for (int k = 0; k < 4; ++k) {
+    const int t = pos + (k >> 1) * 16 + quad * 4 + (k & 1) * 2;
+    const bool a = (t <= hi) & ((t > lo) | (t < sinks)), b = (t + 1 <= hi) & ((t + 1 > lo) | (t + 1 < sinks));
+    w[k] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+__device__ __forceinline__ uint4 and4(uint4 x, uint4 m) { return make_uint4(x.x & m.x, x.y & m.y, x.z & m.z, x.w & m.w); }
 
 // Codes of one word as f16, in the order channel (or token) 0..7.  A nibble n
 // read as an e4m3 number is n * 2^-9 exactly (subnormal up to 7, then the first

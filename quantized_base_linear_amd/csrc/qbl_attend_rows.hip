@@ -33,51 +33,77 @@ namespace {
 
 constexpr int kRowWaves = kManyRows / 32;
 constexpr int kRowThreads = 64 * kRowWaves;
-constexpr int kFar = 1 << 30;  // position of a tile that nobody sees
+constexpr int kFar = 1 << 29;  // position of a tile that is not there
 
 template <int DIM>
 struct RowTiles {
   static constexpr int kNb = DIM / 32;
-  static constexpr int kTiles = DIM == 256 ? 1 : 2;              // per step
+  static constexpr int kTiles = DIM >= 128 ? 1 : 2;              // per step
   static constexpr int kItems = kTiles * 2 * DIM / kRowThreads;  // 16-byte pieces of codes per thread and step
   static constexpr int kHalves = 32 * DIM;                       // of one tile's keys (or values) in LDS
   uint4 code[kItems];
   uint4 scale[kItems][4];  // keys: [0]; values: d and m of two channel blocks
-  int pos[kItems];         // the piece's tile
+};
+
+// A step's tiles: their positions (kFar: not there) and pages, looked up one
+// step before their contents are loaded.
+template <int N>
+struct StepAt {
+  int pos[N], page[N];
+};
+
+// What the mask lets a row at position p see: tokens t <= p with t > p - window
+// or t < sinks.  No window: every t <= p.
+__device__ __forceinline__ int window_start(int p, int win) { return win == 0 ? -kFar : p - win; }
+
+// Where a head's tiles are.
+struct HeadAt {
+  const uint8_t* base;  // page 0
+  int64_t page_bytes;
+  int tile_mask;        // tiles per page - 1
 };
 
 template <int DIM>
-__device__ __forceinline__ void load_step(const KvAttend& a, const Entry& e, const Span& sp, int h, int v, int v1,
-                                          int page_shift, int tid, RowTiles<DIM>& t) {
+__device__ __forceinline__ void find_step(const KvAttend& a, const Entry& e, const Span& sp, int v, int v1, int page_shift,
+                                          StepAt<RowTiles<DIM>::kTiles>& at) {
+#pragma unroll
+  for (int z = 0; z < RowTiles<DIM>::kTiles; ++z) {
+    const int pos = span_pos(sp, min(v + z, v1 - 1));
+    at.page[z] = page_of_uniform(a.kv, e.slot, pos, page_shift);
+    at.pos[z] = v + z < v1 ? pos : kFar;
+  }
+}
+
+template <int DIM>
+__device__ __forceinline__ void load_step(const HeadAt& head, StepAt<RowTiles<DIM>::kTiles>& at, int tid, RowTiles<DIM>& t) {
   using R = RowTiles<DIM>;
   constexpr int kNb = R::kNb;
+#pragma unroll
+  for (int z = 0; z < R::kTiles; ++z)
+    if (at.page[z] < 0) at.pos[z] = kFar;
 #pragma unroll
   for (int i = 0; i < R::kItems; ++i) {
     const int id = tid + i * kRowThreads;
     const int part = __builtin_amdgcn_readfirstlane(id / DIM);  // tile * 2 + (values)
-    const int vt = v + (part >> 1);
-    t.pos[i] = kFar;
-    t.code[i] = make_uint4(0, 0, 0, 0);
+    const int z = R::kTiles - 1;
+    const int pos = part > 1 ? at.pos[z] : at.pos[0], page = part > 1 ? at.page[z] : at.page[0];
+    if (pos == kFar) {
+      t.code[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t.scale[i][k] = make_uint4(0, 0, 0, 0);
-    if (vt >= v1) continue;
-    const int pos = span_pos(sp, vt);
-    const int page = page_of_uniform(a.kv, e.slot, pos, page_shift);
-    if (page < 0) continue;
-    t.pos[i] = pos;
-    const uint8_t* p = tile_ptr<DIM>(a.kv, a.layer, page, h, pos, page_shift);
+      for (int k = 0; k < 4; ++k) t.scale[i][k] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint8_t* p = head.base + page * head.page_bytes + (pos >> 5 & head.tile_mask) * (int)kv_tile_bytes(DIM);
     const int x = id % DIM;
     if (!(part & 1)) {
-      const uint4* kc = reinterpret_cast<const uint4*>(p);
-      const uint8_t* ks = p + 16 * DIM;
       const int tok = x & 31, q = x >> 5;
       if constexpr (DIM == 64) {
-        t.code[i] = kc[tok * 2 + q];
-        const uint2 s = *reinterpret_cast<const uint2*>(ks + tok * 8);
+        t.code[i] = *reinterpret_cast<const uint4*>(p + (tok * 2 + q) * 16);
+        const uint2 s = *reinterpret_cast<const uint2*>(p + 16 * DIM + tok * 8);
         t.scale[i][0] = make_uint4(s.x, s.y, s.x, s.y);
       } else {
-        t.code[i] = kc[((q >> 2) * 32 + tok) * 4 + (q & 3)];
-        t.scale[i][0] = *reinterpret_cast<const uint4*>(ks + (tok * kNb + (q >> 2) * 4) * 4);
+        t.code[i] = *reinterpret_cast<const uint4*>(p + (((q >> 2) * 32 + tok) * 4 + (q & 3)) * 16);
+        t.scale[i][0] = *reinterpret_cast<const uint4*>(p + 16 * DIM + (tok * kNb + (q >> 2) * 4) * 4);
       }
     } else {
       const uint4* vc = reinterpret_cast<const uint4*>(p + 16 * DIM + 128 * kNb);
@@ -92,12 +118,13 @@ __device__ __forceinline__ void load_step(const KvAttend& a, const Entry& e, con
   }
 }
 
-__device__ __forceinline__ bool all_seen(int pos, int first, int last, int win, int sinks) {
-  return pos + 31 <= first && (win == 0 || pos > last - win || pos + 31 < sinks);
+__device__ __forceinline__ bool all_seen(int pos, const Span& sp, int win, int sinks) {
+  return (pos + 31 <= sp.first) & ((pos > window_start(sp.last, win)) | (pos + 31 < sinks));
 }
 
 template <int DIM>
-__device__ __forceinline__ void store_step(RowTiles<DIM>& t, const Span& sp, int win, int sinks, int tid, h8v* lds) {
+__device__ __forceinline__ void store_step(RowTiles<DIM>& t, const StepAt<RowTiles<DIM>::kTiles>& at, const Span& sp, int win,
+                                           int sinks, int tid, h8v* lds) {
   using R = RowTiles<DIM>;
 #pragma unroll
   for (int i = 0; i < R::kItems; ++i) {
@@ -122,9 +149,11 @@ __device__ __forceinline__ void store_step(RowTiles<DIM>& t, const Span& sp, int
       }
     } else {
       const int ln = x & 15, quad = x >> 4 & 3, c64 = x >> 6;
-      if (t.pos[i] != kFar && !all_seen(t.pos[i], sp.first, sp.last, win, sinks)) {
+      const int pos = R::kTiles > 1 && part > 1 ? at.pos[R::kTiles - 1] : at.pos[0];
+      if (!all_seen(pos, sp, win, sinks)) {
+        const uint4 seen = seen_mask(pos, quad, sp.last, window_start(sp.first, win), sinks);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t.scale[i][k] = hide(t.scale[i][k], t.pos[i], quad, sp, win, sinks);
+        for (int k = 0; k < 4; ++k) t.scale[i][k] = and4(t.scale[i][k], seen);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -161,8 +190,22 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   if (splits > 1 && split * chunk >= sp.tiles) return;
   const int v0 = split * chunk, v1 = min(sp.tiles, v0 + chunk);
 
+  HeadAt head;
+  {
+    const int per = 1 << (page_shift - 5);
+    const int64_t tile = (int64_t)kv_tile_bytes(DIM);
+    head.base = static_cast<const uint8_t*>(a.kv.store) +
+                ((int64_t)a.layer * a.kv.n_pages * a.kv.n_kv_heads + h) * per * tile;
+    head.page_bytes = a.kv.n_kv_heads * per * tile;
+    head.tile_mask = per - 1;
+  }
   RowTiles<DIM> t;
-  if (v0 < v1) load_step<DIM>(a, e, sp, h, v0, v1, page_shift, tid, t);
+  StepAt<kTiles> now, in, ahead;  // multiplied, in registers, next to load
+  if (v0 < v1) {
+    find_step<DIM>(a, e, sp, v0, v1, page_shift, now);
+    find_step<DIM>(a, e, sp, v0 + kTiles, v1, page_shift, in);
+    load_step<DIM>(head, now, tid, t);
+  }
 
   // This lane's row and its queries, times a power of two.
   const int r = r0 + wave * 32 + col;
@@ -170,19 +213,23 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   const int pos_j = e.len - e.c + j;
   const bool ok = r < e.c * a.group && pos_j >= sp.first && pos_j <= sp.last;
   const int pos_of = ok ? pos_j : -1;
-  const int64_t row_at = (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] + (int64_t)hq * a.qs[2];
+  // padding rows read the call's first row instead, and drop it
+  const int64_t row_at = ok ? (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] + (int64_t)hq * a.qs[2] : 0;
   h8v q[DIM / 16];
   float cs;
   {
     float x[DIM / 16][8], big = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < DIM / 16; ++ks) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[ks][k] = 0.0f;
-      if (ok) load8<T>(a.q, row_at + ks * 16 + hf * 8, a.vec, x[ks]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[ks][k]));
+      load8<T>(a.q, row_at + ks * 16 + hf * 8, a.vec, x[ks]);
     }
+#pragma unroll
+    for (int ks = 0; ks < DIM / 16; ++ks)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[ks][k] = ok ? x[ks][k] : 0.0f;
+        big = fmaxf(big, fabsf(x[ks][k]));
+      }
     big = fmaxf(big, __shfl_xor(big, 32));
     const int ex = big > 0.0f && big < __builtin_inff() ? min(14 + 127 - (int)(__float_as_uint(big) >> 23), 100) : 0;
     const float sign = a.scale < 0.0f ? -pow2(ex) : pow2(ex);
@@ -201,9 +248,11 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   float m = kNegInf, l = 0.0f;
 
   if (v0 < v1) {
-    store_step<DIM>(t, sp, win, sinks, tid, lds[0]);
-    load_step<DIM>(a, e, sp, h, v0 + kTiles, v1, page_shift, tid, t);
+    store_step<DIM>(t, now, sp, win, sinks, tid, lds[0]);
+    load_step<DIM>(head, in, tid, t);
+    find_step<DIM>(a, e, sp, v0 + 2 * kTiles, v1, page_shift, ahead);
   }
+  const int lo = window_start(pos_of, win);
   __syncthreads();
 
   int buf = 0;
@@ -215,25 +264,32 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
 #pragma unroll
       for (int k = 0; k < 16; ++k) s[z][k] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < DIM / 16; ++ks) s[z] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kt[ks * 64], q[ks], s[z], 0, 0, 0);
+      for (int k0 = 0; k0 < DIM / 16; k0 += 4) {
+        h8v kf[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) kf[ks] = kt[(k0 + ks) * 64];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) s[z] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[ks], q[k0 + ks], s[z], 0, 0, 0);
+      }
     }
+    const StepAt<kTiles> cur = now;
     if (v + kTiles < v1) {
-      store_step<DIM>(t, sp, win, sinks, tid, lds[buf ^ 1]);
-      load_step<DIM>(a, e, sp, h, v + 2 * kTiles, v1, page_shift, tid, t);
+      store_step<DIM>(t, in, sp, win, sinks, tid, lds[buf ^ 1]);
+      now = in;
+      in = ahead;
+      load_step<DIM>(head, in, tid, t);
+      find_step<DIM>(a, e, sp, v + 3 * kTiles, v1, page_shift, ahead);
     }
     float top = kNegInf;
 #pragma unroll
     for (int z = 0; z < kTiles; ++z) {
-      int pos = kFar;
-      if (v + z < v1) {
-        pos = span_pos(sp, v + z);
-        if (page_of_uniform(a.kv, e.slot, pos, page_shift) < 0) pos = kFar;
-      }
-      if (!all_seen(pos, sp.first, sp.last, win, sinks)) {
+      const int pos = cur.pos[z];
+      if (!all_seen(pos, sp, win, sinks)) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int tok = pos + (k >> 2) * 8 + hf * 4 + (k & 3);
-          const bool seen = tok <= pos_of && (win == 0 || pos_of - tok < win || tok < sinks);
+          const bool seen = (tok <= pos_of) & ((tok > lo) | (tok < sinks));
           s[z][k] = seen ? s[z][k] : kNegInf;
         }
       }
@@ -253,17 +309,17 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
     const float ref = m == kNegInf ? 0.0f : m - kBias;
 #pragma unroll
     for (int z = 0; z < kTiles; ++z) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        s[z][k] = __builtin_amdgcn_exp2f(fmaf(s[z][k], cs, -ref));
-        l += s[z][k];
-      }
       const h8v* vt = lds[buf] + (2 * z + 1) * (R::kHalves / 8) + lane;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s[z][k] = __builtin_amdgcn_exp2f(fmaf(s[z][k], cs, -ref));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         h8v p;
 #pragma unroll
         for (int k = 0; k < 8; ++k) p[k] = (_Float16)s[z][(k >> 2) * 8 + w * 4 + (k & 3)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          l = __builtin_amdgcn_fdot2(h2v{p[2 * k], p[2 * k + 1]}, h2v{(_Float16)1.0f, (_Float16)1.0f}, l, false);
 #pragma unroll
         for (int c = 0; c < DIM / 32; ++c) o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vt[(c * 2 + w) * 64], p, o[c], 0, 0, 0);
       }
