@@ -20,7 +20,7 @@ import ctypes
 
 import torch
 
-from . import _SO, QblError, _dev_ptr, _stream, _ws
+from . import _SO, QblError, _dev_ptr
 
 QBL_T_F32, QBL_T_F16, QBL_T_BF16 = 0, 1, 2
 QBL_KV_MAX_ENTRIES = 1024
@@ -103,6 +103,19 @@ class KVCache:
             raise QblError(code, "a page call could not be done; it changed nothing")
 
 
+# The calls below take a few microseconds on the GPU, so their checks are kept short.
+def _stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _ws(ws):
+    if ws is None:
+        return None, 0
+    return _dev_ptr(ws), ws.nbytes
+
+
 def _ints(t, numel, what):
     if t is None:
         return None
@@ -111,15 +124,19 @@ def _ints(t, numel, what):
     return _dev_ptr(t, torch.int32)
 
 
+_Strides = _i64 * 3
+
+
 def _strided(t, shape, what):
     """Data pointer and strides of an activation tensor whose last dimension is contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    *outer, last = t.stride()
+    if last != 1 and shape[-1] > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), (_i64 * 3)(*t.stride()[:-1])
+    return t.data_ptr(), _Strides(*outer)
 
 
 def _dtype(t):
@@ -178,14 +195,14 @@ def qbl_kv_copy(kv: KVCache, src, dst, stream=None) -> None:
 # -- contents --------------------------------------------------------------------------
 def qbl_kv_append(kv: KVCache, layer: int, slots, counts, k, v, stream=None) -> None:
     """k, v: [n][q_len][n_kv_heads][head_dim], float32, float16 or bfloat16."""
-    n, q_len = k.shape[0], k.shape[1]
+    n, q_len = k.shape[:2]
     shape = (n, q_len, kv.n_kv_heads, kv.head_dim)
     if k.dtype != v.dtype:
         raise ValueError("k and v must have one element type")
     kp, ks = _strided(k, shape, "k")
     vp, vs = _strided(v, shape, "v")
     _check(_lib.qbl_kv_append(kv.ptr, layer, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, q_len, kp,
-                              ctypes.addressof(ks), vp, ctypes.addressof(vs), _dtype(k), _stream(stream)))
+                              ks, vp, vs, _dtype(k), _stream(stream)))
 
 
 def qbl_kv_read(kv: KVCache, layer: int, slots, counts, k_out, v_out, stream=None) -> None:
@@ -216,7 +233,7 @@ def attend_workspace(kv: KVCache, n: int, q_len: int, n_heads: int, max_len: int
 def qbl_kv_attend(kv: KVCache, layer: int, slots, counts, q, out, max_len: int, window: int = 0, sinks: int = 0,
                   scale: float = 0.0, ws=None, stream=None) -> None:
     """q, out: [n][q_len][n_heads][head_dim], one element type; scale 0 means 1/sqrt(head_dim)."""
-    n, q_len, heads = q.shape[0], q.shape[1], q.shape[2]
+    n, q_len, heads = q.shape[:3]
     shape = (n, q_len, heads, kv.head_dim)
     if q.dtype != out.dtype:
         raise ValueError("q and out must have one element type")
@@ -224,7 +241,7 @@ def qbl_kv_attend(kv: KVCache, layer: int, slots, counts, q, out, max_len: int, 
     op, os_ = _strided(out, shape, "out")
     wp, wb = _ws(ws)
     _check(_lib.qbl_kv_attend(kv.ptr, layer, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, q_len, heads, qp,
-                              ctypes.addressof(qs), op, ctypes.addressof(os_), _dtype(q), max_len, window, sinks, scale,
+                              qs, op, os_, _dtype(q), max_len, window, sinks, scale,
                               wp, wb, _stream(stream)))
 
 
@@ -245,13 +262,13 @@ def qbl_verify(target, draft, tokens, counts, u, accepted, next_token, ws, strea
     [n][q_len] (None if q_len is 0), u: float32 [n][q_len + 1]; accepted, next_token: int32 [n]."""
     n, q_len, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
     tp, ts = _strided(target, (n, q_len + 1, vocab), "target")
-    dp, ds = (None, (_i64 * 3)(0, 0, 0)) if draft is None else _strided(draft, (n, q_len, vocab), "draft")
+    dp, ds = (None, None) if draft is None else _strided(draft, (n, q_len, vocab), "draft")
     if draft is not None and draft.dtype != target.dtype:
         raise ValueError("target and draft must have one element type")
     if u.numel() != n * (q_len + 1):
         raise ValueError(f"u: expected {n * (q_len + 1)} elements, got {u.numel()}")
     wp, wb = _ws(ws)
-    _check(_lib.qbl_verify(tp, ctypes.addressof(ts), dp, ctypes.addressof(ds), _dtype(target),
+    _check(_lib.qbl_verify(tp, ts, dp, ds, _dtype(target),
                            _ints(tokens, n * q_len, "tokens"), _ints(counts, n, "counts"), _dev_ptr(u, torch.float32), n,
                            q_len, vocab, _ints(accepted, n, "accepted"), _ints(next_token, n, "next_token"), wp, wb,
                            _stream(stream)))

@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kMaxSplits = 1024;
+constexpr int kMaxSplits = 512;  // attend_plan's most
 
 // LDS writes of this wave become visible to its own later reads; no other wave takes part.
 __device__ __forceinline__ void wave_sync() {
@@ -55,7 +55,7 @@ struct TileRegs {
   uint32_t ks[2][kNb];   // its scales
   uint32_t vc[DIM / 16]; // value codes of channel 16 n + col
   uint4 vs;              // row col of the value scales, tokens of quad
-  int pos;               // first token position, or -1: no page
+  int pos;               // first token position
 };
 
 template <int N>
@@ -69,21 +69,22 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N], 
   }
 }
 
+// The tile at pos of page `page` (-1: none, all zeros and far away).
 template <int DIM>
-__device__ __forceinline__ void load_tile(const KvAttend& a, const Entry& e, int pos, int page, int h, int page_shift,
-                                          int lane, TileRegs<DIM>& t) {
+__device__ __forceinline__ void load_tile(const HeadAt& head, int pos, int page, int lane, TileRegs<DIM>& t) {
   constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4;
   const int col = lane & 15, quad = lane >> 4;
-  t.pos = page < 0 ? -1 : pos;
-  t.vs = make_uint4(0, 0, 0, 0);
+  t.pos = pos;
   if (page < 0) {
+    t.pos = kFar;
+    t.vs = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < kNb; ++k) t.kc[0][k] = t.kc[1][k] = t.ks[0][k] = t.ks[1][k] = 0;
 #pragma unroll
     for (int k = 0; k < DIM / 16; ++k) t.vc[k] = 0;
     return;
   }
-  const uint8_t* p = tile_ptr<DIM>(a.kv, a.layer, page, h, pos, page_shift);
+  const uint8_t* p = tile_in<DIM>(head, page, pos);
   const uint32_t* kc = reinterpret_cast<const uint32_t*>(p);
   const uint32_t* ks = reinterpret_cast<const uint32_t*>(p + 16 * DIM);
   const uint32_t* vc = reinterpret_cast<const uint32_t*>(p + 16 * DIM + 128 * kNb);
@@ -95,7 +96,7 @@ __device__ __forceinline__ void load_tile(const KvAttend& a, const Entry& e, int
       load_words<kNb>(kc + ((ch * 32 + half * 16 + col) * 4 + quad) * kNg, t.kc[half], 4 * ch);
       load_words<kNb>(ks + (half * 16 + col) * kNb + 4 * ch, t.ks[half], 4 * ch);
     }
-  if (col < 2 * kNb) t.vs = vs[col * 4 + quad];
+  t.vs = vs[min(col, 2 * kNb - 1) * 4 + quad];  // rows past the last repeat it; their products are not used
 #pragma unroll
   for (int ch = 0; ch < DIM / 64; ++ch) load_words<DIM / 16>(vc + ((ch * 16 + col) * 4 + quad) * 4, t.vc, 4 * ch);
 }
@@ -110,8 +111,12 @@ __device__ __forceinline__ h2v times8(h2v x) { return x * h2v{(_Float16)8.0f, (_
 
 __device__ __forceinline__ f4v mfma(h8v x, h8v y, f4v acc) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, acc, 0, 0, 0); }
 
+// Waves per SIMD that the registers have to leave room for.
 template <int DIM, int T, int NT>
-__global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_blocks, int chunk, int splits,
+constexpr int kMinWaves = DIM == 256 || (DIM == 128 && NT == 2 && T == QBL_T_F32) ? 1 : 2;
+
+template <int DIM, int T, int NT>
+__global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kernel(KvAttend a, int row_blocks, int chunk, int splits,
                                                           int page_shift, int64_t part_floats) {
   constexpr int kNb = DIM / 32;
   constexpr bool kExact = T != QBL_T_BF16;
@@ -139,12 +144,19 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
   const int v1 = min(sp.tiles, (split + 1) * chunk);
   int v = split * chunk + wave;
 
-  auto fetch = [&](int x, TileRegs<DIM>& t) {
-    const int pos = span_pos(sp, x);
-    load_tile<DIM>(a, e, pos, page_of_uniform(a.kv, e.slot, pos, page_shift), h, page_shift, lane, t);
+  const HeadAt head = head_at<DIM>(a, h, page_shift);
+  // Positions and pages are looked up one tile before its contents are loaded.
+  int pos_ahead = kFar, page_ahead = -1;
+  auto find = [&](int x) {
+    pos_ahead = span_pos(sp, min(x, v1 - 1));
+    page_ahead = page_of_uniform(a.kv, e.slot, pos_ahead, page_shift);
   };
   TileRegs<DIM> ta, tb;
-  if (v < v1) fetch(v, ta);
+  if (v < v1) {
+    find(v);
+    load_tile<DIM>(head, pos_ahead, page_ahead, lane, ta);
+    find(v + kWaves);
+  }
 
   h8v q[NT][kNb][kQp], qs[NT][kNb / 4 + 1];  // qs: what the blocks' scales (d, m) x 4 meet, part `quad` of 8*qsum, qsum
   float cs[NT];                              // score factor, in the exponent of 2
@@ -157,16 +169,18 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
     const bool ok = r < e.c * a.group && pos >= sp.first && pos <= sp.last;
     pos_of[nt] = ok ? pos : -1;
     float x[kNb][8], big = 0.0f;
-    const int64_t at = (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] +
-                       (int64_t)(h * a.group + r - j * a.group) * a.qs[2] + quad * 8;
+    // padding rows read the call's first row instead, and drop it
+    const int64_t at = (ok ? (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] +
+                             (int64_t)(h * a.group + r - j * a.group) * a.qs[2] : 0) + quad * 8;
 #pragma unroll
-    for (int g = 0; g < kNb; ++g) {
+    for (int g = 0; g < kNb; ++g) load8<T>(a.q, at + g * 32, a.vec, x[g]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[g][k] = 0.0f;
-      if (ok) load8<T>(a.q, at + g * 32, a.vec, x[g]);
+    for (int g = 0; g < kNb; ++g)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(x[g][k]));
-    }
+      for (int k = 0; k < 8; ++k) {
+        x[g][k] = ok ? x[g][k] : 0.0f;
+        big = fmaxf(big, fabsf(x[g][k]));
+      }
     const int ex = row_exponent(big, 6);
     const float up = a.scale < 0.0f ? -pow2(ex) : pow2(ex);
     cs[nt] = fabsf(a.scale) * kLog2e * pow2(-ex);
@@ -203,25 +217,27 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
     }
   }
 
-  f4v o[NT][DIM / 16], lin[NT];
+  f4v o[NT][DIM / 16], lin[NT], lost[NT];  // lost: what roundings took from lin (float32 rows)
   float m[NT], l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt] = kNegInf, l[nt] = 0.0f;
-    lin[nt] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
+    lin[nt] = lost[nt] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int n = 0; n < DIM / 16; ++n) o[nt][n] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
   }
   uint4* sc = steps[wave];
 
   auto step = [&](TileRegs<DIM>& t, TileRegs<DIM>& next) {
-    if (v + kWaves < v1) fetch(v + kWaves, next);
-    if (t.pos < 0) return;
+    if (v + kWaves < v1) {
+      load_tile<DIM>(head, pos_ahead, page_ahead, lane, next);
+      find(v + 2 * kWaves);
+    }
     const int pos = t.pos;
-    const bool full = pos + 31 <= sp.first && (win == 0 || pos >= sp.last - win + 1 || pos + 31 < sinks);
+    const bool full = all_seen(pos, sp, win, sinks);
     // Value scales of tokens that no row sees become 0, so that whatever is
     // stored there meets a weight of 0 as a finite number.
-    if (!full) t.vs = and4(t.vs, seen_mask(pos, quad, sp.last, win == 0 ? -1 : sp.first - win, sinks));
+    if (!full) t.vs = and4(t.vs, seen_mask(pos, quad, sp.last, window_start(sp.first, win), sinks));
     wave_sync();
     if (col < 2 * kNb) sc[col * 4 + quad] = t.vs;
     wave_sync();
@@ -281,7 +297,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
       for (int k = 0; k < 8; ++k) {
         if (!full) {
           const int tok = pos + (k >> 2) * 16 + quad * 4 + (k & 3);
-          const bool seen = tok <= pos_of[nt] && (win == 0 || pos_of[nt] - tok < win || tok < sinks);
+          const bool seen = (tok <= pos_of[nt]) & ((tok > window_start(pos_of[nt], win)) | (tok < sinks));
           s[nt][k] = seen ? s[nt][k] : kNegInf;
         }
         s[nt][k] *= cs[nt];  // rounded before the subtraction: the largest score's weight is a power of 2
@@ -295,6 +311,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
         m[nt] = up;
         l[nt] *= f;
         lin[nt] *= f;
+        if constexpr (T == QBL_T_F32) lost[nt] *= f;
 #pragma unroll
         for (int n = 0; n < DIM / 16; ++n) o[nt][n] *= f;
       }
@@ -314,9 +331,19 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(KvAttend a, int row_bl
     if constexpr (kExact) {
       const h8v w = __builtin_bit_cast(h8v, t.vs);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (T == QBL_T_F32) {
+          // sum p d and sum p m are large and nearly cancel: compensated sums
+          f4v add = mfma(w, p[nt][0], mfma(w, p[nt][1], f4v{0.0f, 0.0f, 0.0f, 0.0f}));
+          add -= lost[nt];
+          const f4v sum = lin[nt] + add;
+          lost[nt] = (sum - lin[nt]) - add;
+          lin[nt] = sum;
+        } else {
 #pragma unroll
-        for (int z = kPp - 1; z >= 0; --z) lin[nt] = mfma(w, p[nt][z], lin[nt]);
+          for (int z = kPp - 1; z >= 0; --z) lin[nt] = mfma(w, p[nt][z], lin[nt]);
+        }
+      }
     }
 #pragma unroll
     for (int g = 0; g < kNb; ++g) {
@@ -553,15 +580,20 @@ AttendPlan attend_plan(const KvAttend& a) {
   }
   tiles = std::max<int64_t>(tiles, 1);
   const int64_t base = (int64_t)a.rows.n * a.kv.n_kv_heads * p.row_blocks;
-  int64_t want;
+  int64_t want, step = 1;
   if (p.many) {
     // Two workgroups per CU, each at least 8 tiles.
     want = std::min<int64_t>(std::max<int64_t>(1, 512 / base), (tiles + 7) / 8);
   } else {
-    // Enough workgroups to fill the device twice over, each wave at least one tile.
-    want = std::min<int64_t>(std::max<int64_t>(1, 1024 / base), (tiles + kWaves - 1) / kWaves);
+    // Two workgroups per CU, each wave at least one tile.  Requests may be much
+    // shorter than the longest, so up to 16 splits of 64 tiles also where that
+    // many workgroups are there without: 32 requests of 1 to 20000 tokens take
+    // 114 us so, 133 us with the fewest.
+    want = std::max<int64_t>(512 / base, std::min<int64_t>((tiles + 63) / 64, 16));
+    want = std::min<int64_t>(std::max<int64_t>(want, 1), (tiles + kWaves - 1) / kWaves);
+    step = kWaves;
   }
-  p.chunk = (int)((tiles + want - 1) / want);
+  p.chunk = (int)(((tiles + want - 1) / want + step - 1) / step * step);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
   const int64_t out_rows = (int64_t)a.rows.n * a.rows.q_len * a.heads;
   p.ws_bytes = p.splits == 1 ? 0 : out_rows * p.splits * (a.kv.head_dim + 2) * 4;

@@ -78,6 +78,37 @@ __device__ __forceinline__ int page_of_uniform(const qbl_kv& kv, int slot, int p
   return p >= 0 && p < kv.n_pages ? p : -1;
 }
 
+constexpr int kFar = 1 << 29;  // position of a tile that is not there
+
+// Where one head's tiles are.
+struct HeadAt {
+  const uint8_t* base;  // page 0
+  int64_t page_bytes;
+  int tile_mask;        // tiles per page - 1
+};
+
+template <int DIM>
+__device__ __forceinline__ HeadAt head_at(const KvAttend& a, int h, int page_shift) {
+  const int per = 1 << (page_shift - 5);
+  const int64_t tile = kv_tile_bytes(DIM);
+  return HeadAt{static_cast<const uint8_t*>(a.kv.store) + ((int64_t)a.layer * a.kv.n_pages * a.kv.n_kv_heads + h) * per * tile,
+                a.kv.n_kv_heads * per * tile, per - 1};
+}
+
+template <int DIM>
+__device__ __forceinline__ const uint8_t* tile_in(const HeadAt& head, int page, int pos) {
+  return head.base + page * head.page_bytes + (pos >> 5 & head.tile_mask) * (int)kv_tile_bytes(DIM);
+}
+
+// Tokens t <= p with t > window_start(p) or t < sinks are what a row at position
+// p sees.  No window: every t <= p.
+__device__ __forceinline__ int window_start(int p, int win) { return win == 0 ? -kFar : p - win; }
+
+// Every row of the span sees all of the tile at pos.
+__device__ __forceinline__ bool all_seen(int pos, const Span& sp, int win, int sinks) {
+  return (pos + 31 <= sp.first) & ((pos > window_start(sp.last, win)) | (pos + 31 < sinks));
+}
+
 // Which (entry, head) pair and which of its `per` workgroups workgroup b is.
 // The 8 XCDs take workgroups in turn; pair p goes to XCD p % 8, so that the
 // workgroups that read the same part of the cache share an L2.  Pairs past the

@@ -33,7 +33,6 @@ namespace {
 
 constexpr int kRowWaves = kManyRows / 32;
 constexpr int kRowThreads = 64 * kRowWaves;
-constexpr int kFar = 1 << 29;  // position of a tile that is not there
 
 template <int DIM>
 struct RowTiles {
@@ -50,17 +49,6 @@ struct RowTiles {
 template <int N>
 struct StepAt {
   int pos[N], page[N];
-};
-
-// What the mask lets a row at position p see: tokens t <= p with t > p - window
-// or t < sinks.  No window: every t <= p.
-__device__ __forceinline__ int window_start(int p, int win) { return win == 0 ? -kFar : p - win; }
-
-// Where a head's tiles are.
-struct HeadAt {
-  const uint8_t* base;  // page 0
-  int64_t page_bytes;
-  int tile_mask;        // tiles per page - 1
 };
 
 template <int DIM>
@@ -93,7 +81,7 @@ __device__ __forceinline__ void load_step(const HeadAt& head, StepAt<RowTiles<DI
       for (int k = 0; k < 4; ++k) t.scale[i][k] = make_uint4(0, 0, 0, 0);
       continue;
     }
-    const uint8_t* p = head.base + page * head.page_bytes + (pos >> 5 & head.tile_mask) * (int)kv_tile_bytes(DIM);
+    const uint8_t* p = tile_in<DIM>(head, page, pos);
     const int x = id % DIM;
     if (!(part & 1)) {
       const int tok = x & 31, q = x >> 5;
@@ -116,10 +104,6 @@ __device__ __forceinline__ void load_step(const HeadAt& head, StepAt<RowTiles<DI
       t.scale[i][3] = vs[(kNb + 2 * c + 1) * 4 + quad];
     }
   }
-}
-
-__device__ __forceinline__ bool all_seen(int pos, const Span& sp, int win, int sinks) {
-  return (pos + 31 <= sp.first) & ((pos > window_start(sp.last, win)) | (pos + 31 < sinks));
 }
 
 template <int DIM>
@@ -190,15 +174,7 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   if (splits > 1 && split * chunk >= sp.tiles) return;
   const int v0 = split * chunk, v1 = min(sp.tiles, v0 + chunk);
 
-  HeadAt head;
-  {
-    const int per = 1 << (page_shift - 5);
-    const int64_t tile = (int64_t)kv_tile_bytes(DIM);
-    head.base = static_cast<const uint8_t*>(a.kv.store) +
-                ((int64_t)a.layer * a.kv.n_pages * a.kv.n_kv_heads + h) * per * tile;
-    head.page_bytes = a.kv.n_kv_heads * per * tile;
-    head.tile_mask = per - 1;
-  }
+  const HeadAt head = head_at<DIM>(a, h, page_shift);
   RowTiles<DIM> t;
   StepAt<kTiles> now, in, ahead;  // multiplied, in registers, next to load
   if (v0 < v1) {
