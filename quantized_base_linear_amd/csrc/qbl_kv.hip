@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kClamp = 32768.0f;  // keeps d*15 + m inside fp16's range
 
-__device__ __forceinline__ float tame(float x) { return x == x ? fminf(fmaxf(x, -kClamp), kClamp) : 0.0f; }
+__device__ __forceinline__ float tame(float x) { return x == x ? __builtin_amdgcn_fmed3f(x, -kClamp, kClamp) : 0.0f; }
 
 // Quantise 8 of a block's 32 channels; the other 24 are with the three
 // neighbouring lanes (4-lane groups).  Returns the codes as two words of four
@@ -36,15 +36,32 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& lo4
   const float m = __half2float(mh);
   const __half dh = __float2half_rn((hi - m) / 15.0f);
   const float d = __half2float(dh);
+  // The quotient through the reciprocal (2^-22 off, relative) decides the code
+  // unless it is next to a half; then the wave divides, so codes are those of
+  // the division.  (Divisions and their rounding bound the kernel: 10 of its 28
+  // instructions per value.)
+  const float inv = d > 0.0f ? __builtin_amdgcn_rcpf(d) : 0.0f;
+  float edge = 1.0f;
   lo4 = hi4 = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float t = d > 0.0f ? (x[j] - m) / d : 0.0f;
-    t = fminf(fmaxf(t, 0.0f), 15.0f);
-    const float w = floorf(t);
-    const uint32_t code = (uint32_t)w + (t - w >= 0.5f ? 1u : 0u);
+    const float t = (x[j] - m) * inv;
+    edge = fminf(edge, fabsf(__builtin_amdgcn_fractf(t) - 0.5f));
+    const uint32_t code = (uint32_t)(__builtin_amdgcn_fmed3f(t, 0.0f, 15.0f) + 0.5f);
     if (j < 4) lo4 |= code << (8 * j);
     else hi4 |= code << (8 * (j - 4));
+  }
+  if (__any(edge < 1.0f / 32768.0f)) {
+    lo4 = hi4 = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float t = d > 0.0f ? (x[j] - m) / d : 0.0f;
+      t = fminf(fmaxf(t, 0.0f), 15.0f);
+      const float w = floorf(t);
+      const uint32_t code = (uint32_t)w + (t - w >= 0.5f ? 1u : 0u);
+      if (j < 4) lo4 |= code << (8 * j);
+      else hi4 |= code << (8 * (j - 4));
+    }
   }
   return (uint32_t)__half_as_ushort(dh) | (uint32_t)__half_as_ushort(mh) << 16;
 }
@@ -73,18 +90,29 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend a, int pag
   uint32_t* kc = reinterpret_cast<uint32_t*>(tile);
   uint32_t* ks = reinterpret_cast<uint32_t*>(tile + 16 * DIM);
   uint16_t* vs = reinterpret_cast<uint16_t*>(tile + 32 * DIM + 128 * kNb);
-  for (int w0 = 0; w0 < 2 * work; w0 += kThreads) {
-    const int w = w0 + tid;
+  // All of a thread's values are loaded before the first is needed.
+  constexpr int kSteps = 8 * DIM / kThreads;
+  float all[kSteps][8];
+#pragma unroll
+  for (int it = 0; it < kSteps; ++it) {
+    if (it * kThreads >= 2 * work) break;
+    const int w = it * kThreads + tid;
+    const bool val = w >= work;
+    const int x = w < 2 * work ? (val ? w - work : w) : 0;
+    const int quad = x & 3, g = (x >> 2) % kNb, t = t0 + (x >> 2) / kNb;
+    const int64_t* st = val ? a.vs : a.ks;
+    const int64_t at = (int64_t)i * st[0] + (int64_t)(j0 + t) * st[1] + (int64_t)h * st[2] + g * 32 + quad * 8;
+    load8<T>(val ? a.v : a.k, at, a.vec, all[it]);
+  }
+#pragma unroll
+  for (int it = 0; it < kSteps; ++it) {
+    if (it * kThreads >= 2 * work) break;
+    const int w = it * kThreads + tid;
     const bool live = w < 2 * work;
     const bool val = w >= work;
     const int x = live ? (val ? w - work : w) : 0;
     const int quad = x & 3, g = (x >> 2) % kNb, t = t0 + (x >> 2) / kNb;
-    float f[8];
-    {
-      const int64_t* st = val ? a.vs : a.ks;
-      const int64_t at = (int64_t)i * st[0] + (int64_t)(j0 + t) * st[1] + (int64_t)h * st[2] + g * 32 + quad * 8;
-      load8<T>(val ? a.v : a.k, at, a.vec, f);
-    }
+    float (&f)[8] = all[it];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = tame(f[j]);
     uint32_t lo4, hi4;
@@ -110,6 +138,14 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend a, int pag
     const int n = w & 3, quad = (w >> 2) & 3, lane = (w >> 4) & 15, chunk = w >> 8;
     const int ch = chunk * 64 + n * 16 + lane;
     uint32_t word = 0, mask = 0;
+    if (t0 == 0 && t1 == 32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        word |= (uint32_t)cb[(quad * 4 + j) * kRow + ch] << (8 * j) |
+                (uint32_t)cb[(16 + quad * 4 + j) * kRow + ch] << (8 * j + 4);
+      vc[w] = word;
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int ta = quad * 4 + j, tb = 16 + ta;
@@ -122,7 +158,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend a, int pag
   }
 }
 
-// One workgroup per 8 rows of one head: a thread per 8 channels of a row.
+// Few rows per entry: a thread per 8 channels of a row, which picks its value
+// codes byte by byte.
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(qbl_kv kv, int layer, KvRows rows, float* k_out, float* v_out,
                                                            int page_shift) {
@@ -166,6 +203,73 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(qbl_kv kv, int layer,
   vo[1] = make_float4(vx[4], vx[5], vx[6], vx[7]);
 }
 
+// Many rows: one workgroup per tile of one head of one entry.  The value codes
+// are read as they lie and turned in LDS.  Rows without a token are 0.
+template <int DIM>
+__global__ __launch_bounds__(kThreads) void kv_read_tile_kernel(qbl_kv kv, int layer, KvRows rows, float* k_out,
+                                                                float* v_out, int page_shift) {
+  constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4, kPer = DIM / 8;
+  constexpr int kRow = DIM + 4;
+  __shared__ uint32_t codes[32 * kRow / 4];
+  const int h = blockIdx.y, i = blockIdx.z, tid = threadIdx.x;
+  const Entry e = load_entry(kv, rows, i);
+  const int start = e.len - e.c;                         // position of row 0; below 0: more new than held
+  const int base = ((start >> 5) + (int)blockIdx.x) * 32;
+  const int j0 = base - start;                           // row of the tile's token 0
+  if (j0 >= rows.q_len) return;
+  const int page = e.c > 0 && base >= 0 && base < e.len ? page_of(kv, e.slot, base, page_shift) : -1;
+  const uint8_t* tile = page < 0 ? nullptr : tile_ptr<DIM>(kv, layer, page, h, base, page_shift);
+  if (page >= 0) {
+    uint8_t* cb = reinterpret_cast<uint8_t*>(codes);
+    const uint4* vc = reinterpret_cast<const uint4*>(tile + 16 * DIM + 128 * kNb);
+    if (tid < DIM) {
+      const int quad = tid & 3, ln = tid >> 2 & 15, chunk = tid >> 6;
+      const uint4 w4 = vc[tid];
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          cb[((j >> 2) * 16 + quad * 4 + (j & 3)) * kRow + chunk * 64 + n * 16 + ln] =
+              (uint8_t)(w[n] >> (8 * (j & 3) + 4 * (j >> 2)) & 15u);
+    }
+    __syncthreads();  // the whole workgroup has the same page
+  }
+#pragma unroll
+  for (int it = 0; it < 32 * kPer / kThreads; ++it) {
+    const int x = it * kThreads + tid;
+    const int part = x % kPer, quad = part & 3, g = part >> 2, t = x / kPer;
+    const int j = j0 + t;
+    if (j < 0 || j >= rows.q_len) continue;
+    float kx[8], vx[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) kx[c] = vx[c] = 0.0f;
+    if (page >= 0 && j < e.c) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(tile)[((g / kNg * 32 + t) * 4 + quad) * kNg + g % kNg];
+      const uint32_t dm = reinterpret_cast<const uint32_t*>(tile + 16 * DIM)[t * kNb + g];
+      const uint16_t* vs = reinterpret_cast<const uint16_t*>(tile + 32 * DIM + 128 * kNb);
+      const int s = (g * 4 + (t & 15) / 4) * 8 + (t >> 4) * 4 + (t & 3);
+      const float kd = half_bits(dm & 0xFFFFu), km = half_bits(dm >> 16);
+      const float vd = half_bits(vs[s]), vm = half_bits(vs[32 * kNb + s]);
+      const uint32_t v4[2] = {codes[(t * kRow + g * 32 + quad * 8) / 4], codes[(t * kRow + g * 32 + quad * 8) / 4 + 1]};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        kx[c] = fmaf(kd, (float)((w >> (8 * (c & 3) + 4 * (c >> 2))) & 15u), km);
+        vx[c] = fmaf(vd, (float)(v4[c >> 2] >> (8 * (c & 3)) & 15u), vm);
+      }
+    }
+    const int64_t at = (((int64_t)i * rows.q_len + j) * kv.n_kv_heads + h) * DIM + g * 32 + quad * 8;
+    float4* ko = reinterpret_cast<float4*>(k_out + at);
+    float4* vo = reinterpret_cast<float4*>(v_out + at);
+    ko[0] = make_float4(kx[0], kx[1], kx[2], kx[3]);
+    ko[1] = make_float4(kx[4], kx[5], kx[6], kx[7]);
+    vo[0] = make_float4(vx[0], vx[1], vx[2], vx[3]);
+    vo[1] = make_float4(vx[4], vx[5], vx[6], vx[7]);
+  }
+}
+
+constexpr int kFewRows = 16;  // rows per entry up to which rows are read one by one
+
 int page_shift_of(const qbl_kv& kv) { return __builtin_ctz((unsigned)kv.page_tokens); }
 
 template <int DIM>
@@ -181,6 +285,11 @@ hipError_t append_dim(const KvAppend& a, const LaunchCtx& lc) {
 
 template <int DIM>
 hipError_t read_dim(const qbl_kv& kv, int layer, const KvRows& rows, float* k_out, float* v_out, const LaunchCtx& lc) {
+  if (rows.q_len > kFewRows) {
+    const dim3 grid((unsigned)((rows.q_len + 30) / 32 + 1), (unsigned)kv.n_kv_heads, (unsigned)rows.n);
+    QBL_LAUNCH(kv_read_tile_kernel<DIM>, grid, dim3(kThreads), 0, lc, kv, layer, rows, k_out, v_out, page_shift_of(kv));
+    return hipGetLastError();
+  }
   constexpr int kRows = kThreads / (DIM / 8);
   const dim3 grid((unsigned)((rows.q_len + kRows - 1) / kRows), (unsigned)kv.n_kv_heads, (unsigned)rows.n);
   QBL_LAUNCH(kv_read_kernel<DIM>, grid, dim3(kThreads), 0, lc, kv, layer, rows, k_out, v_out, page_shift_of(kv));

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kWg = 1024;
 constexpr int kWaves = kWg / 64;
-constexpr int kPiece = 16384;  // bytes of a page that one workgroup copies at a time
+constexpr int kPiece = 8192;  // bytes of a page that one workgroup copies at a time
 
 // Exclusive prefix sum over the workgroup; total receives the sum.  `red`:
 // kWaves + 1 words of LDS.
@@ -71,11 +71,17 @@ __device__ __forceinline__ int entry_of(const int* start, int n, int x) {
   return lo;
 }
 
-// True when slot s (entry i) is also listed by an earlier entry.
-__device__ __forceinline__ bool listed_before(const int* slot, int i, int s) {
-  for (int j = 0; j < i; ++j)
-    if (slot[j] == s) return true;
-  return false;
+// How many of the entries before i have value s.  Four at a time, without an
+// early exit, so that the reads overlap: the list is short but every thread
+// goes through it.  `list`: 16-byte aligned, kWg entries.
+__device__ __forceinline__ int listed_before(const int* list, int i, int s) {
+  int found = 0;
+#pragma unroll 4
+  for (int j = 0; j < i; j += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(list + j);
+    found += (v.x == s) + (j + 1 < i && v.y == s) + (j + 2 < i && v.z == s) + (j + 3 < i && v.w == s);
+  }
+  return found;
 }
 
 // 16 consecutive refs from page p (those past n_pages read as used).
@@ -98,7 +104,8 @@ __device__ __forceinline__ unsigned free_mask16(const qbl_kv& kv, int p) {
 
 __global__ __launch_bounds__(kWg) void extend_kernel(qbl_kv kv, const int32_t* slots, const int32_t* counts, int n,
                                                      PagesWs ws) {
-  __shared__ int slot_of[kWg], last_of[kWg], first_new[kWg], start[kWg];
+  __shared__ __align__(16) int slot_of[kWg], last_of[kWg];
+  __shared__ int first_new[kWg], start[kWg];
   __shared__ int red[kWaves + 1];
   __shared__ unsigned word;
   const int i = threadIdx.x, pt = kv.page_tokens;
@@ -117,7 +124,7 @@ __global__ __launch_bounds__(kWg) void extend_kernel(qbl_kv kv, const int32_t* s
   int have = 0, need = 0, last = -1;
   bool part = false;
   if (i < n && err == 0) {
-    if (listed_before(slot_of, i, s)) err = QBL_E_DUPLICATE;
+    if (listed_before(slot_of, i, s) > 0) err = QBL_E_DUPLICATE;
     else if ((int64_t)len + add > (int64_t)kv.max_pages * pt) err = QBL_E_LIMIT;
     else {
       have = (len + pt - 1) >> sh;
@@ -136,11 +143,7 @@ __global__ __launch_bounds__(kWg) void extend_kernel(qbl_kv kv, const int32_t* s
   bool copy = false;
   if (part) {
     const int r = kv.refs[last];
-    if (r > 1) {
-      int earlier = 0;
-      for (int j = 0; j < i; ++j) earlier += last_of[j] == last;
-      copy = r - earlier > 1;
-    }
+    if (r > 1) copy = r - listed_before(last_of, i, last) > 1;
   }
   int bad = block_error(err, &word);
   if (bad) {
@@ -202,7 +205,8 @@ __global__ __launch_bounds__(kWg) void extend_kernel(qbl_kv kv, const int32_t* s
 
 __global__ __launch_bounds__(kWg) void fork_kernel(qbl_kv kv, const int32_t* src, const int32_t* dst,
                                                    const int32_t* prefix, int n) {
-  __shared__ int from[kWg], to[kWg], start[kWg];
+  __shared__ __align__(16) int to[kWg];
+  __shared__ int from[kWg], start[kWg];
   __shared__ int red[kWaves + 1];
   __shared__ unsigned word;
   const int i = threadIdx.x, pt = kv.page_tokens;
@@ -212,7 +216,7 @@ __global__ __launch_bounds__(kWg) void fork_kernel(qbl_kv kv, const int32_t* src
   if (i < n) {
     const int s = from[i], d = to[i];
     if (s < 0 || s >= kv.n_slots || d < 0 || d >= kv.n_slots) err = QBL_E_ARG;
-    else if (listed_before(to, i, d)) err = QBL_E_DUPLICATE;
+    else if (listed_before(to, i, d) > 0) err = QBL_E_DUPLICATE;
     else if (kv.lens[d] > 0) err = QBL_E_STATE;
     else {
       len = min(max(kv.lens[s], 0), kv.max_pages * pt);
@@ -242,7 +246,8 @@ __global__ __launch_bounds__(kWg) void fork_kernel(qbl_kv kv, const int32_t* src
 }
 
 __global__ __launch_bounds__(kWg) void truncate_kernel(qbl_kv kv, const int32_t* slots, const int32_t* lens, int n) {
-  __shared__ int slot_of[kWg], first[kWg], start[kWg];
+  __shared__ __align__(16) int slot_of[kWg];
+  __shared__ int first[kWg], start[kWg];
   __shared__ int red[kWaves + 1];
   __shared__ unsigned word;
   const int i = threadIdx.x, pt = kv.page_tokens;
@@ -254,7 +259,7 @@ __global__ __launch_bounds__(kWg) void truncate_kernel(qbl_kv kv, const int32_t*
   }
   __syncthreads();
   if (i < n && err == 0) {
-    if (listed_before(slot_of, i, s)) err = QBL_E_DUPLICATE;
+    if (listed_before(slot_of, i, s) > 0) err = QBL_E_DUPLICATE;
     else {
       len = min(max(kv.lens[s], 0), kv.max_pages * pt);
       keep = min(max(lens[i], 0), len);
@@ -330,27 +335,30 @@ __global__ __launch_bounds__(kWg) void compact_plan_kernel(qbl_kv kv, PagesWs ws
   if (i == 0) ws.head[0] = holes, ws.head[1] = used;
 }
 
-__global__ __launch_bounds__(256) void remap_kernel(qbl_kv kv, const int32_t* map) {
-  const int64_t all = (int64_t)kv.n_slots * kv.max_pages, stride = (int64_t)gridDim.x * 256;
-  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += stride) {
-    const int p = kv.table[x];
-    if (p >= 0 && p < kv.n_pages) {
-      const int to = map[p];
-      if (to != p) kv.table[x] = to;
+// Copies `count` pages (the device word if given, else n) in all layers.  With
+// `map`, the tables' pages are renamed by it first (a compaction: the two touch
+// different memory).
+__global__ __launch_bounds__(256) void copy_pages_kernel(qbl_kv kv, const int32_t* src, const int32_t* dst,
+                                                         const int32_t* count, int n, int64_t page_bytes,
+                                                         const int32_t* map) {
+  if (map) {
+    const int64_t all = (int64_t)kv.n_slots * kv.max_pages, stride = (int64_t)gridDim.x * 256;
+    for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += stride) {
+      const int p = kv.table[x];
+      if (p >= 0 && p < kv.n_pages) {
+        const int to = map[p];
+        if (to != p) kv.table[x] = to;
+      }
     }
   }
-}
-
-// Copies `count` pages (the device word if given, else n) in all layers.
-__global__ __launch_bounds__(256) void copy_pages_kernel(qbl_kv kv, const int32_t* src, const int32_t* dst,
-                                                         const int32_t* count, int n, int64_t page_bytes) {
   const int pairs = count ? min(*count, n) : n;
-  const int pieces = (int)((page_bytes + kPiece - 1) / kPiece);
-  const int64_t units = (int64_t)pairs * kv.n_layers * pieces;
+  const unsigned pieces = (unsigned)((page_bytes + kPiece - 1) / kPiece), per = pieces * (unsigned)kv.n_layers;
+  const int64_t units = (int64_t)pairs * per;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int piece = (int)(u % pieces);
-    const int64_t pl = u / pieces;
-    const int layer = (int)(pl % kv.n_layers), pair = (int)(pl / kv.n_layers);
+    // units past 2^32 need the long division
+    const int pair = units >> 32 ? (int)(u / per) : (int)((unsigned)u / per);
+    const unsigned rest = (unsigned)(u - (int64_t)pair * per);
+    const int layer = (int)(rest / pieces), piece = (int)(rest - layer * pieces);
     const int from = src[pair], to = dst[pair];
     if (from < 0 || from >= kv.n_pages || to < 0 || to >= kv.n_pages) continue;
     const int64_t off = (int64_t)piece * kPiece;
@@ -370,14 +378,23 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(qbl_kv kv, const int32_
 
 }  // namespace
 
-hipError_t launch_kv_copy(const qbl_kv& kv, const int32_t* src, const int32_t* dst, const int32_t* count, int n,
-                          const LaunchCtx& lc) {
-  (void)hipGetLastError();  // drop errors left by earlier, unrelated calls
+namespace {
+
+hipError_t copy_pages(const qbl_kv& kv, const int32_t* src, const int32_t* dst, const int32_t* count, int n,
+                      const int32_t* map, const LaunchCtx& lc) {
   const int64_t bytes = qbl_kv_page_bytes(kv.page_tokens, kv.n_kv_heads, kv.head_dim);
   const int64_t units = (int64_t)n * kv.n_layers * ((bytes + kPiece - 1) / kPiece);
   const int grid = (int)std::min<int64_t>(units, 2048);
-  QBL_LAUNCH(copy_pages_kernel, dim3(grid), dim3(256), 0, lc, kv, src, dst, count, n, bytes);
+  QBL_LAUNCH(copy_pages_kernel, dim3(grid), dim3(256), 0, lc, kv, src, dst, count, n, bytes, map);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_copy(const qbl_kv& kv, const int32_t* src, const int32_t* dst, const int32_t* count, int n,
+                          const LaunchCtx& lc) {
+  (void)hipGetLastError();  // drop errors left by earlier, unrelated calls
+  return copy_pages(kv, src, dst, count, n, nullptr, lc);
 }
 
 hipError_t launch_kv_extend(const qbl_kv& kv, const int32_t* slots, const int32_t* counts, int n, const PagesWs& ws,
@@ -406,13 +423,9 @@ hipError_t launch_kv_truncate(const qbl_kv& kv, const int32_t* slots, const int3
 hipError_t launch_kv_compact(const qbl_kv& kv, const PagesWs& ws, const LaunchCtx& lc) {
   (void)hipGetLastError();
   QBL_LAUNCH(compact_plan_kernel, dim3(1), dim3(kWg), 0, lc, kv, ws);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t all = (int64_t)kv.n_slots * kv.max_pages;
-  QBL_LAUNCH(remap_kernel, dim3((unsigned)std::min<int64_t>((all + 255) / 256, 1024)), dim3(256), 0, lc, kv, ws.map);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_kv_copy(kv, ws.src, ws.dst, ws.head, kv.n_pages, lc);
+  return copy_pages(kv, ws.src, ws.dst, ws.head, kv.n_pages, ws.map, lc);
 }
 
 }  // namespace qbl

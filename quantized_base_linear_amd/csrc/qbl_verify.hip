@@ -6,13 +6,15 @@
 // read per request, once, so the work is bound by memory for many requests and
 // by launch latency for one.
 //
-// First launch: workgroups of one 4096-token piece each find a (a few loads,
-// repeated by every workgroup of the request) and sum their piece of w and of p
-// in float64.  Second launch: one workgroup per request finds the piece that
-// the draw falls into from those sums and reads that piece again.  Differences
-// of two float32 values and their products are exact in float64, and sums of a
-// row are within 2^-35 of exact, so the drawn token does not depend on the
-// order of summation except with that probability.
+// First launch: workgroups of one piece (1024 or 4096 tokens) each find a (a few
+// loads, repeated by every workgroup of the request) and sum their piece of w
+// and of p in float64.  Second launch: one workgroup per request finds the piece
+// that the draw falls into from those sums and reads that piece again.
+// Differences of two float32 values are exact in float64, and sums of a row are
+// within 2^-35 of exact, so the drawn token does not depend on the order of
+// summation except with that probability.  (One workgroup per request that does
+// all in one launch was slower, 16 us against 12 for 32000 tokens: one CU draws
+// 256 KB at some 25 GB/s only.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -23,11 +25,14 @@ namespace qbl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 4096;
-constexpr int kPer = kPiece / kThreads;
+// Tokens per workgroup of the first launch: small pieces spread few rows over
+// the device, large ones save repeating the decision where there are many.
+constexpr int kSmall = 1024, kLarge = 4096;
+int piece_of(int n, int vocab) { return (int64_t)n * vocab <= 2048ll * kSmall ? kSmall : kLarge; }
 
 // A usable probability: finite and positive, anything else counts as 0.
-__device__ __forceinline__ double weight(float x) { return x > 0.0f && x < __builtin_inff() ? (double)x : 0.0; }
+__device__ __forceinline__ float usable(float x) { return x > 0.0f && x < __builtin_inff() ? x : 0.0f; }
+__device__ __forceinline__ double weight(float x) { return (double)usable(x); }
 
 struct Draw {
   int a;         // accepted tokens
@@ -35,22 +40,29 @@ struct Draw {
   int token;     // the rejected token
 };
 
-// Every thread of the workgroup receives the request's outcome (kThreads >=
-// QBL_KV_MAX_DRAFT: a thread per drafted token).
+// Every thread of the workgroup receives the request's outcome (at least
+// QBL_KV_MAX_DRAFT threads: one per drafted token).
 template <int T>
 __device__ __forceinline__ Draw accept(const VerifyArgs& v, int b) {
-  __shared__ int first;
-  const int c = v.counts ? min(max(v.counts[b], 0), v.q_len) : v.q_len;
+  __shared__ int first, token;
   const int j = threadIdx.x;
-  if (j == 0) first = c;
+  // what does not depend on another load is loaded together
+  const int given = v.counts ? v.counts[b] : v.q_len;
+  int x = -1;
+  float u = 0.0f;
+  if (j < v.q_len) {
+    x = v.tokens[(int64_t)b * v.q_len + j];
+    u = v.u[(int64_t)b * (v.q_len + 1) + j];
+  }
+  const int c = min(max(given, 0), v.q_len);
+  if (j == 0) first = c, token = -1;
   __syncthreads();
   if (j < c) {
-    const int x = v.tokens[(int64_t)b * v.q_len + j];
     bool ok = x >= 0 && x < v.vocab;
     if (ok) {
       const double p = weight(load_elem<T>(v.target, b * v.ts[0] + j * v.ts[1] + x));
       const double q = v.draft ? weight(load_elem<T>(v.draft, b * v.ds[0] + j * v.ds[1] + x)) : 1.0;
-      ok = (double)v.u[(int64_t)b * (v.q_len + 1) + j] * q < p;
+      ok = (double)u * q < p;
     }
     if (!ok) atomicMin(&first, j);
   }
@@ -58,7 +70,9 @@ __device__ __forceinline__ Draw accept(const VerifyArgs& v, int b) {
   Draw d;
   d.a = first;
   d.rejected = d.a < c;
-  d.token = d.rejected ? v.tokens[(int64_t)b * v.q_len + d.a] : -1;
+  if (j == d.a && d.rejected) token = x;
+  __syncthreads();
+  d.token = token;
   return d;
 }
 
@@ -79,15 +93,67 @@ __device__ __forceinline__ double wave_sum64(double x) {
   return x;
 }
 
-template <int T>
+// Inclusive sums over the wave's lanes.
+__device__ __forceinline__ double wave_scan64(double x) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const double y = __shfl_up(x, s);
+    if ((int)(threadIdx.x & 63) >= s) x += y;
+  }
+  return x;
+}
+
+// The workgroup (W waves) looks through the 64 W PER tokens from t0: the first
+// whose running sum of w (p where `use_p`) passes the goal, or the last with
+// any weight, or -1, for thread 0.
+template <int T, int PER, int W>
+__device__ __forceinline__ int locate(const VerifyArgs& v, int b, const Draw& d, bool use_p, int t0, double goal) {
+  __shared__ double red[W];
+  __shared__ int hit, last;
+  const int tid = threadIdx.x;
+  if (tid == 0) hit = v.vocab, last = -1;
+  double w[PER], mine = 0.0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int t = t0 + tid * PER + k;
+    w[k] = 0.0;
+    if (t < v.vocab) {
+      double p, x;
+      weights<T>(v, b, d, t, p, x);
+      w[k] = use_p ? p : x;
+    }
+    mine += w[k];
+  }
+  const double upto = wave_scan64(mine);
+  if ((tid & 63) == 63) red[tid >> 6] = upto;
+  __syncthreads();
+  double c = upto - mine;
+#pragma unroll
+  for (int k = 0; k < W; ++k) c += k < (tid >> 6) ? red[k] : 0.0;
+  int first = v.vocab, end = -1;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    c += w[k];
+    if (w[k] > 0.0) {
+      end = t0 + tid * PER + k;
+      if (first == v.vocab && c > goal) first = end;
+    }
+  }
+  if (first < v.vocab) atomicMin(&hit, first);
+  if (end >= 0) atomicMax(&last, end);
+  __syncthreads();
+  return hit < v.vocab ? hit : last;
+}
+
+template <int T, int PIECE>
 __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs v, int pieces) {
   __shared__ double red[2][kThreads / 64];
   const int b = blockIdx.y, piece = blockIdx.x;
   const Draw d = accept<T>(v, b);
   double sw = 0.0, sp = 0.0;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int t = piece * kPiece + k * kThreads + threadIdx.x;
+  for (int k = 0; k < PIECE / kThreads; ++k) {
+    const int t = piece * PIECE + k * kThreads + threadIdx.x;
     if (t < v.vocab) {
       double p, w;
       weights<T>(v, b, d, t, p, w);
@@ -102,92 +168,76 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs v, int 
     for (int w = 0; w < kThreads / 64; ++w) s += red[threadIdx.x][w];
     v.ws[((int64_t)b * pieces + piece) * 2 + threadIdx.x] = s;
   }
+  if (piece == 0 && threadIdx.x == 0)
+    reinterpret_cast<int4*>(v.ws + (int64_t)v.n * pieces * 2)[b] = make_int4(d.a, d.rejected, d.token, 0);
 }
 
-template <int T>
-__global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyArgs v, int pieces) {
-  __shared__ double red[kThreads / 64];
-  __shared__ int hit, last, chosen, which;
+template <int T, int PIECE>
+__global__ __launch_bounds__(PIECE / 4) void verify_pick_kernel(VerifyArgs v, int pieces) {
+  __shared__ int chosen, which;
   __shared__ double before;
   const int b = blockIdx.x, tid = threadIdx.x;
-  const Draw d = accept<T>(v, b);
   const double* sums = v.ws + (int64_t)b * pieces * 2;
-  if (tid == 0) {
-    double tw = 0.0, tp = 0.0;
-    for (int k = 0; k < pieces; ++k) tw += sums[2 * k], tp += sums[2 * k + 1];
-    const int use = tw > 0.0 ? 0 : 1;  // nothing left of p - q: draw from p
-    const double goal = (double)v.u[(int64_t)b * (v.q_len + 1) + v.q_len] * (use ? tp : tw);
+  const int4 kept = reinterpret_cast<const int4*>(v.ws + (int64_t)v.n * pieces * 2)[b];
+  const float draw = v.u[(int64_t)b * (v.q_len + 1) + v.q_len];
+  const Draw d = {kept.x, kept.y, kept.z};
+  if (tid < 64) {
+    // The total, then the first piece whose running sum passes the goal (the last
+    // piece with any weight, if none does): 64 pieces at a time.
+    const double mine = tid < pieces ? sums[2 * tid] : 0.0;
+    double all = mine;
+    for (int k = tid + 64; k < pieces; k += 64) all += sums[2 * k];
+    all = wave_sum64(all);
+    const int use = all > 0.0 ? 0 : 1;  // nothing left of p - q: draw from p
+    if (use) {
+      for (int k = tid; k < pieces; k += 64) all += sums[2 * k + 1];
+      all = wave_sum64(all);
+    }
+    const double goal = (double)draw * all;
     double c = 0.0, at = 0.0;
     int pick = -1;
-    for (int k = 0; k < pieces; ++k) {
-      const double s = sums[2 * k + use];
-      if (s > 0.0) pick = k, at = c;  // the last piece with any weight, if none passes the goal
-      c += s;
-      if (s > 0.0 && c > goal) break;
+    for (int k0 = 0; k0 < pieces; k0 += 64) {
+      const double s = k0 == 0 && !use ? mine : k0 + tid < pieces ? sums[2 * (k0 + tid) + use] : 0.0;
+      const double upto = c + wave_scan64(s);
+      const uint64_t some = __ballot(s > 0.0), hits = __ballot(s > 0.0 && upto > goal);
+      const uint64_t from = hits ? hits & -hits : some;
+      if (from) {
+        const int lane = 63 - __clzll(from);
+        pick = k0 + lane;
+        at = __shfl(upto - s, lane);
+      }
+      if (hits) break;
+      c = __shfl(upto, 63);
     }
-    chosen = pick, which = use, before = goal - at;
-    hit = v.vocab, last = -1;
+    if (tid == 0) chosen = pick, which = use, before = goal - at;
   }
   __syncthreads();
-  const int pick = chosen;
-  if (pick >= 0) {
-    const double goal = before;
-    double w[kPer], mine = 0.0;
-    const int t0 = pick * kPiece + tid * kPer;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      w[k] = 0.0;
-      if (t0 + k < v.vocab) {
-        double p, x;
-        weights<T>(v, b, d, t0 + k, p, x);
-        w[k] = which ? p : x;
-      }
-      mine += w[k];
-    }
-    // exclusive prefix over the workgroup
-    double x = mine;
-    const int lane = tid & 63;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const double y = __shfl_up(x, s);
-      if (lane >= s) x += y;
-    }
-    if (lane == 63) red[tid >> 6] = x;
-    __syncthreads();
-    double c = x - mine;
-    for (int k = 0; k < (tid >> 6); ++k) c += red[k];
-    int first = v.vocab, end = -1;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      c += w[k];
-      if (w[k] > 0.0) {
-        end = t0 + k;
-        if (first == v.vocab && c > goal) first = t0 + k;
-      }
-    }
-    if (first < v.vocab) atomicMin(&hit, first);
-    if (end >= 0) atomicMax(&last, end);
-  }
-  __syncthreads();
-  if (tid == 0) {
-    v.accepted[b] = d.a;
-    v.next[b] = hit < v.vocab ? hit : last;
-  }
+  const int next = chosen < 0 ? -1 : locate<T, 4, PIECE / 256>(v, b, d, which != 0, chosen * PIECE, before);
+  if (tid == 0) v.accepted[b] = d.a, v.next[b] = next;
+}
+
+template <int T, int PIECE>
+hipError_t launch_piece(const VerifyArgs& a, const LaunchCtx& lc) {
+  const int pieces = (a.vocab + PIECE - 1) / PIECE;
+  QBL_LAUNCH((verify_sum_kernel<T, PIECE>), dim3((unsigned)pieces, (unsigned)a.n), dim3(kThreads), 0, lc, a, pieces);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  QBL_LAUNCH((verify_pick_kernel<T, PIECE>), dim3((unsigned)a.n), dim3(PIECE / 4), 0, lc, a, pieces);
+  return hipGetLastError();
 }
 
 template <int T>
 hipError_t launch_type(const VerifyArgs& a, const LaunchCtx& lc) {
-  const int pieces = (a.vocab + kPiece - 1) / kPiece;
-  QBL_LAUNCH(verify_sum_kernel<T>, dim3((unsigned)pieces, (unsigned)a.n), dim3(kThreads), 0, lc, a, pieces);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  QBL_LAUNCH(verify_pick_kernel<T>, dim3((unsigned)a.n), dim3(kThreads), 0, lc, a, pieces);
-  return hipGetLastError();
+  return piece_of(a.n, a.vocab) == kSmall ? launch_piece<T, kSmall>(a, lc) : launch_piece<T, kLarge>(a, lc);
 }
 
 }  // namespace
 
-int64_t verify_ws_bytes(int n, int vocab) { return (int64_t)n * ((vocab + kPiece - 1) / kPiece) * 2 * 8; }
+// Each piece's sums of w and of p, then each request's Draw.
+int64_t verify_ws_bytes(int n, int vocab) {
+  const int piece = piece_of(n, vocab);
+  return (int64_t)n * ((int64_t)((vocab + piece - 1) / piece) * 16 + 16);
+}
 
 hipError_t launch_verify(const VerifyArgs& a, const LaunchCtx& lc) {
   (void)hipGetLastError();  // drop errors left by earlier, unrelated calls
