@@ -168,7 +168,8 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
     const int pos = e.len - e.c + j;
     const bool ok = r < e.c * a.group && pos >= sp.first && pos <= sp.last;
     pos_of[nt] = ok ? pos : -1;
-    float x[kNb][8], big = 0.0f;
+    float x[kNb][8];
+    uint32_t big = 0;
     // padding rows read the call's first row instead, and drop it
     const int64_t at = (ok ? (int64_t)i * a.qs[0] + (int64_t)j * a.qs[1] +
                              (int64_t)(h * a.group + r - j * a.group) * a.qs[2] : 0) + quad * 8;
@@ -179,11 +180,12 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         x[g][k] = ok ? x[g][k] : 0.0f;
-        big = fmaxf(big, fabsf(x[g][k]));
+        big = max(big, magnitude(x[g][k]));
       }
-    const int ex = row_exponent(big, 6);
-    const float up = a.scale < 0.0f ? -pow2(ex) : pow2(ex);
-    cs[nt] = fabsf(a.scale) * kLog2e * pow2(-ex);
+    float up, down;
+    row_factor<true>(big, 6, up, down);
+    if (a.scale < 0.0f) up = -up;
+    cs[nt] = fabsf(a.scale) * kLog2e * down;
 #pragma unroll
     for (int g = 0; g < kNb; ++g) {
       float sum = 0.0f;
@@ -402,6 +404,7 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
     float ls = l[nt];
     ls += __shfl_xor(ls, 16);
     ls += __shfl_xor(ls, 32);
+    if (ls != ls) m[nt] = 0.0f;  // NaN scores raise no maximum: the row must not look unseen
     if (nt > 0) __syncthreads();
 #pragma unroll
     for (int n = 0; n < DIM / 16; ++n) *reinterpret_cast<f4v*>(&obuf[wave][col][n * 16 + quad * 4]) = o[nt][n];

@@ -25,13 +25,20 @@ constexpr float kBias = 11.0f, kRaise = 4.0f;
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// Exponent that brings a row's largest magnitude into [2^top, 2^(top+1)) (less
-// where all of the row is tiny; 0 for a row of zeros or one that is not
-// finite).  `big` is this lane's part; lanes l, l^16 and l^32 share a row.
-__device__ __forceinline__ int row_exponent(float big, int top) {
-  big = fmaxf(big, __shfl_xor(big, 16));
-  big = fmaxf(big, __shfl_xor(big, 32));
-  return big > 0.0f && big < __builtin_inff() ? min(top + 127 - (int)(__float_as_uint(big) >> 23), 100) : 0;
+// Magnitude as an integer that orders like it: NaN above infinity above all others.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Factor of a row whose largest magnitude is `big` (this lane's part; lanes l
+// and l^32 share a row, and with FOUR l^16 too): the power of two `up` that brings it into [2^top,
+// 2^(top+1)) (less where all of the row is tiny, 1 for zeros), and 1/up.  A row
+// that is not finite gets up = NaN: all of its scores, and so its output, are NaN.
+template <bool FOUR>
+__device__ __forceinline__ void row_factor(uint32_t big, int top, float& up, float& down) {
+  if (FOUR) big = max(big, (uint32_t)__shfl_xor((int)big, 16));
+  big = max(big, (uint32_t)__shfl_xor((int)big, 32));
+  const int ex = big == 0 || big >= 0x7F800000u ? 0 : min(top + 127 - (int)(big >> 23), 100);
+  up = big >= 0x7F800000u ? __builtin_nanf("") : pow2(ex);
+  down = pow2(-ex);
 }
 
 // Which halves of a row of value scales (tokens 4 quad + 0..3 and 16 + 4 quad +

@@ -194,7 +194,8 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   h8v q[DIM / 16];
   float cs;
   {
-    float x[DIM / 16][8], big = 0.0f;
+    float x[DIM / 16][8], up, down;
+    uint32_t big = 0;
 #pragma unroll
     for (int ks = 0; ks < DIM / 16; ++ks) {
       load8<T>(a.q, row_at + ks * 16 + hf * 8, a.vec, x[ks]);
@@ -204,16 +205,15 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         x[ks][k] = ok ? x[ks][k] : 0.0f;
-        big = fmaxf(big, fabsf(x[ks][k]));
+        big = max(big, magnitude(x[ks][k]));
       }
-    big = fmaxf(big, __shfl_xor(big, 32));
-    const int ex = big > 0.0f && big < __builtin_inff() ? min(14 + 127 - (int)(__float_as_uint(big) >> 23), 100) : 0;
-    const float sign = a.scale < 0.0f ? -pow2(ex) : pow2(ex);
+    row_factor<false>(big, 14, up, down);
+    if (a.scale < 0.0f) up = -up;
 #pragma unroll
     for (int ks = 0; ks < DIM / 16; ++ks)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[ks][k] = (_Float16)(x[ks][k] * sign);
-    cs = fabsf(a.scale) * kLog2e * pow2(-ex);
+      for (int k = 0; k < 8; ++k) q[ks][k] = (_Float16)(x[ks][k] * up);
+    cs = fabsf(a.scale) * kLog2e * down;
   }
 
   f16v o[DIM / 32];
@@ -304,6 +304,7 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   }
 
   l += __shfl_xor(l, 32);
+  if (l != l) m = 0.0f;  // NaN scores raise no maximum: the row must not look unseen
   if (r >= a.rows.q_len * a.group) return;
   if (splits == 1) {
     const bool none = !ok || m == kNegInf;
