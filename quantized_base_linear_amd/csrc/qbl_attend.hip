@@ -69,13 +69,13 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N], 
   }
 }
 
-// The tile at pos of page `page` (-1: none, all zeros and far away).
+// The tile at pos of page `page` (none there: all zeros and far away).
 template <int DIM>
-__device__ __forceinline__ void load_tile(const HeadAt& head, int pos, int page, int lane, TileRegs<DIM>& t) {
+__device__ __forceinline__ void load_tile(const HeadAt& head, int pos, int page, bool there, int lane, TileRegs<DIM>& t) {
   constexpr int kNb = DIM / 32, kNg = kNb < 4 ? kNb : 4;
   const int col = lane & 15, quad = lane >> 4;
   t.pos = pos;
-  if (page < 0) {
+  if (!there) {
     t.pos = kFar;
     t.vs = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -149,12 +149,12 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
   int pos_ahead = kFar, page_ahead = -1;
   auto find = [&](int x) {
     pos_ahead = span_pos(sp, min(x, v1 - 1));
-    page_ahead = page_of_uniform(a.kv, e.slot, pos_ahead, page_shift);
+    page_ahead = table_entry(a.kv, e.slot, pos_ahead, page_shift);
   };
   TileRegs<DIM> ta, tb;
   if (v < v1) {
     find(v);
-    load_tile<DIM>(head, pos_ahead, page_ahead, lane, ta);
+    load_tile<DIM>(head, pos_ahead, page_ahead, is_page(a.kv, page_ahead), lane, ta);
     find(v + kWaves);
   }
 
@@ -232,10 +232,10 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
 
   auto step = [&](TileRegs<DIM>& t, TileRegs<DIM>& next) {
     if (v + kWaves < v1) {
-      load_tile<DIM>(head, pos_ahead, page_ahead, lane, next);
+      load_tile<DIM>(head, pos_ahead, page_ahead, is_page(a.kv, page_ahead), lane, next);
       find(v + 2 * kWaves);
     }
-    const int pos = t.pos;
+    const int pos = __builtin_amdgcn_readfirstlane(t.pos);
     const bool full = all_seen(pos, sp, win, sinks);
     // Value scales of tokens that no row sees become 0, so that whatever is
     // stored there meets a weight of 0 as a finite number.
@@ -294,14 +294,18 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
     h8v p[NT][kPp];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      if (!full) {
+        const int lo = window_start(pos_of[nt], win);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int tok = pos + (k >> 2) * 16 + quad * 4 + (k & 3);
+          const bool seen = (tok <= pos_of[nt]) & ((tok > lo) | (tok < sinks));
+          s[nt][k] = seen ? s[nt][k] : kNegInf;
+        }
+      }
       float top = kNegInf;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (!full) {
-          const int tok = pos + (k >> 2) * 16 + quad * 4 + (k & 3);
-          const bool seen = (tok <= pos_of[nt]) & ((tok > window_start(pos_of[nt], win)) | (tok < sinks));
-          s[nt][k] = seen ? s[nt][k] : kNegInf;
-        }
         s[nt][k] *= cs[nt];  // rounded before the subtraction: the largest score's weight is a power of 2
         top = fmaxf(top, s[nt][k]);
       }

@@ -77,13 +77,16 @@ __device__ __forceinline__ h2v as_h2(uint32_t w) { return __builtin_bit_cast(h2v
 __device__ __forceinline__ h2v low2(uint32_t w) { return as_h2(__builtin_amdgcn_perm(w, w, 0x01000100u)); }
 __device__ __forceinline__ h2v high2(uint32_t w) { return as_h2(__builtin_amdgcn_perm(w, w, 0x03020302u)); }
 
-// Page of a slot's position through the scalar cache (the table is not written
-// by the kernels that use this): uniform arguments give a scalar load.
-__device__ __forceinline__ int page_of_uniform(const qbl_kv& kv, int slot, int pos, int page_shift) {
+// The table's entry for a slot's position through the scalar cache (the table is
+// not written by the kernels that use this): uniform arguments give a scalar
+// load.  Whether it is a page is checked where it is used (is_page), so that
+// nothing waits for the load here.
+__device__ __forceinline__ int table_entry(const qbl_kv& kv, int slot, int pos, int page_shift) {
   typedef const __attribute__((address_space(4))) int32_t* cptr;
-  const int p = ((cptr)(uintptr_t)(kv.table + (int64_t)slot * kv.max_pages))[pos >> page_shift];
-  return p >= 0 && p < kv.n_pages ? p : -1;
+  return ((cptr)(uintptr_t)(kv.table + (int64_t)slot * kv.max_pages))[pos >> page_shift];
 }
+
+__device__ __forceinline__ bool is_page(const qbl_kv& kv, int p) { return (unsigned)p < (unsigned)kv.n_pages; }
 
 constexpr int kFar = 1 << 29;  // position of a tile that is not there
 

@@ -57,18 +57,18 @@ __device__ __forceinline__ void find_step(const KvAttend& a, const Entry& e, con
 #pragma unroll
   for (int z = 0; z < RowTiles<DIM>::kTiles; ++z) {
     const int pos = span_pos(sp, min(v + z, v1 - 1));
-    at.page[z] = page_of_uniform(a.kv, e.slot, pos, page_shift);
+    at.page[z] = table_entry(a.kv, e.slot, pos, page_shift);
     at.pos[z] = v + z < v1 ? pos : kFar;
   }
 }
 
 template <int DIM>
-__device__ __forceinline__ void load_step(const HeadAt& head, StepAt<RowTiles<DIM>::kTiles>& at, int tid, RowTiles<DIM>& t) {
+__device__ __forceinline__ void load_step(const qbl_kv& kv, const HeadAt& head, StepAt<RowTiles<DIM>::kTiles>& at, int tid, RowTiles<DIM>& t) {
   using R = RowTiles<DIM>;
   constexpr int kNb = R::kNb;
 #pragma unroll
   for (int z = 0; z < R::kTiles; ++z)
-    if (at.page[z] < 0) at.pos[z] = kFar;
+    if (!is_page(kv, at.page[z])) at.pos[z] = kFar;
 #pragma unroll
   for (int i = 0; i < R::kItems; ++i) {
     const int id = tid + i * kRowThreads;
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   if (v0 < v1) {
     find_step<DIM>(a, e, sp, v0, v1, page_shift, now);
     find_step<DIM>(a, e, sp, v0 + kTiles, v1, page_shift, in);
-    load_step<DIM>(head, now, tid, t);
+    load_step<DIM>(a.kv, head, now, tid, t);
   }
 
   // This lane's row and its queries, times a power of two.
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
 
   if (v0 < v1) {
     store_step<DIM>(t, now, sp, win, sinks, tid, lds[0]);
-    load_step<DIM>(head, in, tid, t);
+    load_step<DIM>(a.kv, head, in, tid, t);
     find_step<DIM>(a, e, sp, v0 + 2 * kTiles, v1, page_shift, ahead);
   }
   const int lo = window_start(pos_of, win);
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
       store_step<DIM>(t, in, sp, win, sinks, tid, lds[buf ^ 1]);
       now = in;
       in = ahead;
-      load_step<DIM>(head, in, tid, t);
+      load_step<DIM>(a.kv, head, in, tid, t);
       find_step<DIM>(a, e, sp, v + 3 * kTiles, v1, page_shift, ahead);
     }
     float top = kNegInf;
