@@ -7,9 +7,10 @@
 //   float32 and f16 rows: no key or value is rounded.  With d = dh + dl (7 and
 //   4 significant bits) the products (code - 8)*dh and (code - 8)*dl are exact
 //   f16 numbers, and the rest of a block is linear in its scales:
-//     score(t, q)  = c * [ sum_k (dh + dl)(code - 8) q_k + sum_g (8 d + m)(t,g) * qsum_g ]
 //     out(q, ch)  ~  sum_t p_t (dh + dl)(code - 8) + sum_t p_t (8 d + m)(t,g),  g = ch / 32.
-//   The last terms are matrix products too, whose operands are the scales as
+//   Scores the same way with 32 rows; with 16 rows
+//     score(t, q)  = c * sum_g [ d(t,g) sum_k code q_k + m(t,g) * qsum_g ].
+//   The linear terms are matrix products too, whose operands are the scales as
 //   they are stored.  Queries (float32) and weights enter as two f16 parts.
 //   bf16 rows: x is rounded once to f16 (2^-12 relative, against the output's
 //   2^-9), the weights too.
@@ -46,6 +47,16 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int N>
+__device__ __forceinline__ void store_words(uint32_t* p, const uint32_t (&w)[N]) {
+  if constexpr (N == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) *reinterpret_cast<uint4*>(p + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+  }
 }
 
 template <int DIM>
@@ -120,10 +131,16 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
                                                           int page_shift, int64_t part_floats) {
   constexpr int kNb = DIM / 32;
   constexpr bool kExact = T != QBL_T_BF16;
+  // Where the keys' steps enter: with 16 rows after the product, in float32
+  // (fewer instructions per tile: 56.5 -> 50 us for one float32 row over 131071
+  // tokens); with 32 rows that costs more registers than there are, and they
+  // enter through dh and dl, as the values' do.
+  constexpr bool kAfter = kExact && NT == 1;
   constexpr int kQp = T == QBL_T_F32 ? 2 : 1;  // f16 parts of q
   constexpr int kPp = kExact ? 2 : 1;          // f16 parts of the weights
   constexpr int kOut = DIM + 4;
   __shared__ uint4 steps[kWaves][8 * kNb];
+  __shared__ __align__(16) uint32_t kscales[kAfter ? kWaves : 1][kAfter ? 32 * kNb : 4];
   __shared__ __align__(16) float obuf[kWaves][16][kOut];
   __shared__ float linear[kWaves][16][17];
   __shared__ float ml[kWaves][16][2];
@@ -209,7 +226,7 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
           sum -= (float)y;
           part = quad == p ? y : part;
         }
-        qs[nt][g / 4][2 * (g % 4)] = part * (_Float16)8.0f;
+        qs[nt][g / 4][2 * (g % 4)] = kAfter ? (_Float16)0.0f : part * (_Float16)8.0f;
         qs[nt][g / 4][2 * (g % 4) + 1] = part;
       }
     }
@@ -229,6 +246,7 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
     for (int n = 0; n < DIM / 16; ++n) o[nt][n] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
   }
   uint4* sc = steps[wave];
+  uint32_t* kd = kscales[kAfter ? wave : 0];
 
   auto step = [&](TileRegs<DIM>& t, TileRegs<DIM>& next) {
     if (v + kWaves < v1) {
@@ -242,6 +260,10 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
     if (!full) t.vs = and4(t.vs, seen_mask(pos, quad, sp.last, window_start(sp.first, win), sinks));
     wave_sync();
     if (col < 2 * kNb) sc[col * 4 + quad] = t.vs;
+    if constexpr (kAfter) {
+      if (quad == 0) store_words<kNb>(kd + col * kNb, t.ks[0]);
+      if (quad == 1) store_words<kNb>(kd + (16 + col) * kNb, t.ks[1]);
+    }
     wave_sync();
 
     float s[NT][8];
@@ -251,6 +273,7 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[nt] = f4v{0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (kExact) {
+        // the blocks' linear terms
 #pragma unroll
         for (int c = 0; c < (kNb + 3) / 4; ++c) {
           uint4 w = make_uint4(t.ks[half][4 * c], t.ks[half][4 * c + 1], 0, 0);
@@ -259,12 +282,33 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
           for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(__builtin_bit_cast(h8v, w), qs[nt][c], acc[nt]);
         }
       }
+      if constexpr (kAfter) {
+        // Each block's sum of codes times its step; this lane's rows of the product
+        // are tokens 4 quad + 0..3.
+        uint32_t dm[4 * kNb];
 #pragma unroll
-      for (int g = 0; g < kNb; ++g) {
-        h2v c[4], x[4];
-        codes8(t.kc[half][g], c);
-        const h2v d = low2(t.ks[half][g]);
-        if constexpr (kExact) {
+        for (int z = 0; z < kNb; ++z)
+          *reinterpret_cast<uint4*>(dm + 4 * z) = reinterpret_cast<const uint4*>(kd + (half * 16 + quad * 4) * kNb)[z];
+#pragma unroll
+        for (int g = 0; g < kNb; ++g) {
+          h2v c[4];
+          codes8(t.kc[half][g], c);
+          const h8v code = join8(c);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            f4v sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int p = kQp - 1; p >= 0; --p) sum = mfma(code, q[nt][g][p], sum);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[nt][r] = fmaf((float)as_h2(dm[r * kNb + g])[0], sum[r], acc[nt][r]);
+          }
+        }
+      } else if constexpr (kExact) {
+#pragma unroll
+        for (int g = 0; g < kNb; ++g) {
+          h2v c[4], x[4];
+          codes8(t.kc[half][g], c);
+          const h2v d = low2(t.ks[half][g]);
           h2v dh, dl;
           split_step(__builtin_bit_cast(uint32_t, d), dh, dl);
 #pragma unroll
@@ -277,12 +321,17 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int p = kQp - 1; p >= 0; --p) acc[nt] = mfma(hi, q[nt][g][p], mfma(lo, q[nt][g][p], acc[nt]));
-        } else {
-          const h2v mm = high2(t.ks[half][g]);
+        }
+      } else {
 #pragma unroll
-          for (int z = 0; z < 4; ++z) x[z] = __builtin_elementwise_fma(c[z], d, mm);
+        for (int g = 0; g < kNb; ++g) {
+          h2v c[4];
+          codes8(t.kc[half][g], c);
+          const h2v d = low2(t.ks[half][g]), mm = high2(t.ks[half][g]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(join8(x), q[nt][g][0], acc[nt]);
+          for (int z = 0; z < 4; ++z) c[z] = __builtin_elementwise_fma(c[z], d, mm);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(join8(c), q[nt][g][0], acc[nt]);
         }
       }
 #pragma unroll
