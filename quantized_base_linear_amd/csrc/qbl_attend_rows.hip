@@ -41,7 +41,7 @@ struct RowTiles {
   static constexpr int kItems = kTiles * 2 * DIM / kRowThreads;  // 16-byte pieces of codes per thread and step
   static constexpr int kHalves = 32 * DIM;                       // of one tile's keys (or values) in LDS
   uint4 code[kItems];
-  uint4 scale[kItems][4];  // keys: [0]; values: d and m of two channel blocks
+  uint4 scale[kItems][2];  // keys: [0]; values: d and m of one channel block
 };
 
 // A step's tiles: their positions (kFar: not there) and pages, looked up one
@@ -78,7 +78,7 @@ __device__ __forceinline__ void load_step(const qbl_kv& kv, const HeadAt& head, 
     if (pos == kFar) {
       t.code[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) t.scale[i][k] = make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 2; ++k) t.scale[i][k] = make_uint4(0, 0, 0, 0);
       continue;
     }
     const uint8_t* p = tile_in<DIM>(head, page, pos);
@@ -94,14 +94,15 @@ __device__ __forceinline__ void load_step(const qbl_kv& kv, const HeadAt& head, 
         t.scale[i][0] = *reinterpret_cast<const uint4*>(p + 16 * DIM + (tok * kNb + (q >> 2) * 4) * 4);
       }
     } else {
-      const uint4* vc = reinterpret_cast<const uint4*>(p + 16 * DIM + 128 * kNb);
+      // words of block g of lanes ln and ln + 8
+      const uint2* vc = reinterpret_cast<const uint2*>(p + 16 * DIM + 128 * kNb);
       const uint4* vs = reinterpret_cast<const uint4*>(p + 32 * DIM + 128 * kNb);
-      const int ln = x & 15, quad = x >> 4 & 3, c = x >> 6;
-      t.code[i] = vc[(c * 16 + ln) * 4 + quad];
-      t.scale[i][0] = vs[(2 * c) * 4 + quad];
-      t.scale[i][1] = vs[(2 * c + 1) * 4 + quad];
-      t.scale[i][2] = vs[(kNb + 2 * c) * 4 + quad];
-      t.scale[i][3] = vs[(kNb + 2 * c + 1) * 4 + quad];
+      const int ln = x & 7, quad = x >> 3 & 3, g = x >> 5;
+      const uint2 lo = vc[(((g >> 1) * 16 + ln) * 4 + quad) * 2 + (g & 1)];
+      const uint2 hi = vc[(((g >> 1) * 16 + ln + 8) * 4 + quad) * 2 + (g & 1)];
+      t.code[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      t.scale[i][0] = vs[g * 4 + quad];
+      t.scale[i][1] = vs[(kNb + g) * 4 + quad];
     }
   }
 }
@@ -132,23 +133,23 @@ __device__ __forceinline__ void store_step(RowTiles<DIM>& t, const StepAt<RowTil
         dst[f * 32 + tok] = join8(c);
       }
     } else {
-      const int ln = x & 15, quad = x >> 4 & 3, c64 = x >> 6;
+      const int ln = x & 7, quad = x >> 3 & 3, g = x >> 5;
       const int pos = R::kTiles > 1 && part > 1 ? at.pos[R::kTiles - 1] : at.pos[0];
       if (!all_seen(pos, sp, win, sinks)) {
         const uint4 seen = seen_mask(pos, quad, sp.last, window_start(sp.first, win), sinks);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t.scale[i][k] = and4(t.scale[i][k], seen);
+        for (int k = 0; k < 2; ++k) t.scale[i][k] = and4(t.scale[i][k], seen);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         h2v c[4];
         codes8(w[k], c);
-        const uint4 d = t.scale[i][k >> 1], m = t.scale[i][2 + (k >> 1)];
+        const uint4 d = t.scale[i][0], m = t.scale[i][1];
         c[0] = __builtin_elementwise_fma(c[0], as_h2(d.x), as_h2(m.x));
         c[1] = __builtin_elementwise_fma(c[1], as_h2(d.y), as_h2(m.y));
         c[2] = __builtin_elementwise_fma(c[2], as_h2(d.z), as_h2(m.z));
         c[3] = __builtin_elementwise_fma(c[3], as_h2(d.w), as_h2(m.w));
-        dst[((2 * c64 + (k >> 1)) * 4 + quad) * 32 + 16 * (k & 1) + ln] = join8(c);
+        dst[(g * 4 + quad) * 32 + 16 * (k & 1) + 8 * (k >> 1) + ln] = join8(c);
       }
     }
   }
