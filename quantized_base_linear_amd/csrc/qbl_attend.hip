@@ -41,6 +41,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxSplits = 512;  // attend_plan's most
+constexpr int kFewSplits = 16;   // of a row that one wave may join (at most 64)
 
 // LDS writes of this wave become visible to its own later reads; no other wave takes part.
 __device__ __forceinline__ void wave_sync() {
@@ -577,9 +578,56 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(KvAttend a, int c
   store4<T>(a.out, at, a.ovec, y);
 }
 
+// Joins up to 64 splits: one query row per wave, a lane per split's factor.
+template <int DIM, int T>
+__global__ __launch_bounds__(kThreads) void attend_join_few_kernel(KvAttend a, int cols, int chunk, int splits,
+                                                                   int64_t part_floats) {
+  constexpr int kPer = DIM / 64;
+  const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= (int64_t)a.rows.n * a.rows.q_len * a.heads) return;
+  const int hq = (int)(row % a.heads);
+  const int64_t ij = row / a.heads;
+  const int j = (int)(ij % a.rows.q_len), i = (int)(ij / a.rows.q_len);
+  const Entry e = load_entry(a.kv, a.rows, i);
+  const int r = j * a.group + hq % a.group;
+  const Span sp = row_span(e, r / cols * cols, cols, a.group, (int)a.max_len, (int)a.window, (int)a.sinks);
+  const int pos = e.len - e.c + j;
+  const int used = j < e.c && pos >= sp.first && pos <= sp.last ? (sp.tiles + chunk - 1) / chunk : 0;
+  const float2 st = lane < used ? reinterpret_cast<const float2*>(a.ws + part_floats)[row * splits + lane]
+                                : make_float2(kNegInf, 0.0f);
+  float top = st.x;
+#pragma unroll
+  for (int z = 32; z >= 1; z >>= 1) top = fmaxf(top, __shfl_xor(top, z));
+  const float f = st.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
+  float total = f * st.y;
+#pragma unroll
+  for (int z = 32; z >= 1; z >>= 1) total += __shfl_xor(total, z);
+  float x[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) x[k] = 0.0f;
+  const float* src = a.ws + row * splits * DIM + lane * kPer;
+#pragma unroll 8
+  for (int s = 0; s < used; ++s) {
+    const float fs = __shfl(f, s);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) x[k] = fmaf(fs, src[(int64_t)s * DIM + k], x[k]);
+  }
+  const int64_t at = (int64_t)i * a.os[0] + (int64_t)j * a.os[1] + (int64_t)hq * a.os[2] + lane * kPer;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) store_elem<T>(a.out, at + k, top == kNegInf ? 0.0f : x[k] / total);
+}
+
 template <int DIM, int T>
 hipError_t launch_join(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
   const int64_t rows = (int64_t)a.rows.n * a.rows.q_len * a.heads;
+  // With many rows of few splits a wave per row (2048 rows of 7 splits: 1.6 us
+  // less), else a workgroup per row (32 rows of 7 splits: 1.3 us less).
+  if (p.splits <= kFewSplits && rows >= 1024) {
+    QBL_LAUNCH((attend_join_few_kernel<DIM, T>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, lc, a,
+               p.cols, p.chunk, p.splits, attend_part_floats(a, p));
+    return hipGetLastError();
+  }
   QBL_LAUNCH((attend_join_kernel<DIM, T>), dim3((unsigned)rows), dim3(kThreads), 0, lc, a, p.cols, p.chunk, p.splits,
              attend_part_floats(a, p));
   return hipGetLastError();

@@ -107,52 +107,44 @@ __device__ __forceinline__ void load_step(const qbl_kv& kv, const HeadAt& head, 
   }
 }
 
+// Dequantises word k of a thread's piece i into LDS, in two parts: the codes c,
+// then the values.  x: the piece's index in the tile's keys or values.
 template <int DIM>
-__device__ __forceinline__ void store_step(RowTiles<DIM>& t, const StepAt<RowTiles<DIM>::kTiles>& at, const Span& sp, int win,
-                                           int sinks, int tid, h8v* lds) {
-  using R = RowTiles<DIM>;
+__device__ __forceinline__ uint32_t word_of(const RowTiles<DIM>& t, int i, int k) {
+  const uint32_t w[4] = {t.code[i].x, t.code[i].y, t.code[i].z, t.code[i].w};
+  return w[k];
+}
+
+template <int DIM>
+__device__ __forceinline__ void store_key(const RowTiles<DIM>& t, int i, int k, int x, h2v (&c)[4], h8v* dst) {
+  const int tok = x & 31, q = x >> 5;
+  const uint32_t s[4] = {t.scale[i][0].x, t.scale[i][0].y, t.scale[i][0].z, t.scale[i][0].w};
+  const h2v d = low2(s[k]), m = high2(s[k]);
 #pragma unroll
-  for (int i = 0; i < R::kItems; ++i) {
-    const int id = tid + i * kRowThreads;
-    const int part = __builtin_amdgcn_readfirstlane(id / DIM);
-    const int x = id % DIM;
-    h8v* dst = lds + part * (R::kHalves / 8);
-    const uint32_t w[4] = {t.code[i].x, t.code[i].y, t.code[i].z, t.code[i].w};
-    if (!(part & 1)) {
-      const int tok = x & 31, q = x >> 5;
-      const uint32_t s[4] = {t.scale[i][0].x, t.scale[i][0].y, t.scale[i][0].z, t.scale[i][0].w};
+  for (int z = 0; z < 4; ++z) c[z] = __builtin_elementwise_fma(c[z], d, m);
+  // eighth of the channels: 4 * block + quad
+  const int f = DIM == 64 ? 4 * (k & 1) + 2 * q + (k >> 1) : 4 * ((q >> 2) * 4 + k) + (q & 3);
+  dst[f * 32 + tok] = join8(c);
+}
+
+template <int DIM>
+__device__ __forceinline__ void store_value(const RowTiles<DIM>& t, int i, int k, int x, h2v (&c)[4], h8v* dst) {
+  const int ln = x & 7, quad = x >> 3 & 3, g = x >> 5;
+  const uint4 d = t.scale[i][0], m = t.scale[i][1];
+  c[0] = __builtin_elementwise_fma(c[0], as_h2(d.x), as_h2(m.x));
+  c[1] = __builtin_elementwise_fma(c[1], as_h2(d.y), as_h2(m.y));
+  c[2] = __builtin_elementwise_fma(c[2], as_h2(d.z), as_h2(m.z));
+  c[3] = __builtin_elementwise_fma(c[3], as_h2(d.w), as_h2(m.w));
+  dst[(g * 4 + quad) * 32 + 16 * (k & 1) + 8 * (k >> 1) + ln] = join8(c);
+}
+
+// Scales of tokens that no row of the workgroup sees become 0.
+template <int DIM>
+__device__ __forceinline__ void hide_values(RowTiles<DIM>& t, int i, int x, int pos, const Span& sp, int win, int sinks) {
+  if (all_seen(pos, sp, win, sinks)) return;
+  const uint4 seen = seen_mask(pos, x >> 3 & 3, sp.last, window_start(sp.first, win), sinks);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h2v c[4];
-        codes8(w[k], c);
-        const h2v d = low2(s[k]), m = high2(s[k]);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) c[z] = __builtin_elementwise_fma(c[z], d, m);
-        // eighth of the channels: 4 * block + quad
-        const int f = DIM == 64 ? 4 * (k & 1) + 2 * q + (k >> 1) : 4 * ((q >> 2) * 4 + k) + (q & 3);
-        dst[f * 32 + tok] = join8(c);
-      }
-    } else {
-      const int ln = x & 7, quad = x >> 3 & 3, g = x >> 5;
-      const int pos = R::kTiles > 1 && part > 1 ? at.pos[R::kTiles - 1] : at.pos[0];
-      if (!all_seen(pos, sp, win, sinks)) {
-        const uint4 seen = seen_mask(pos, quad, sp.last, window_start(sp.first, win), sinks);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) t.scale[i][k] = and4(t.scale[i][k], seen);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h2v c[4];
-        codes8(w[k], c);
-        const uint4 d = t.scale[i][0], m = t.scale[i][1];
-        c[0] = __builtin_elementwise_fma(c[0], as_h2(d.x), as_h2(m.x));
-        c[1] = __builtin_elementwise_fma(c[1], as_h2(d.y), as_h2(m.y));
-        c[2] = __builtin_elementwise_fma(c[2], as_h2(d.z), as_h2(m.z));
-        c[3] = __builtin_elementwise_fma(c[3], as_h2(d.w), as_h2(m.w));
-        dst[(g * 4 + quad) * 32 + 16 * (k & 1) + 8 * (k >> 1) + ln] = join8(c);
-      }
-    }
-  }
+  for (int k = 0; k < 2; ++k) t.scale[i][k] = and4(t.scale[i][k], seen);
 }
 
 template <int DIM, int T>
@@ -224,8 +216,26 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
     for (int k = 0; k < 16; ++k) o[c][k] = 0.0f;
   float m = kNegInf, l = 0.0f;
 
+  auto keys = [&](int buf, int z) { return lds[buf] + (2 * z) * (R::kHalves / 8); };
+  auto values = [&](int buf, int z) { return lds[buf] + (2 * z + 1) * (R::kHalves / 8); };
+  // A wave's pieces are keys or values of one tile, except with 256 channels: both.
+  static_assert(R::kItems == (DIM == 256 ? 2 : 1));
+  const int part0 = __builtin_amdgcn_readfirstlane(tid / DIM), tile0 = part0 >> 1;
+  auto pos_in = [&](const StepAt<kTiles>& at) { return kTiles > 1 && tile0 > 0 ? at.pos[kTiles - 1] : at.pos[0]; };
+  // Part n of 2 * words of dequantising this wave's pieces into buffer `buf`.
+  h2v code[4];
+  auto dequantise = [&](int n, int buf, bool key_wave) {
+    const int w = n >> 1, i = DIM == 256 ? w >> 2 : 0, k = w & 3;
+    if (!(n & 1)) codes8(word_of<DIM>(t, i, k), code);
+    else if (DIM == 256 ? w < 4 : key_wave) store_key<DIM>(t, i, k, tid % DIM, code, keys(buf, DIM == 256 ? 0 : tile0));
+    else store_value<DIM>(t, i, k, tid % DIM, code, values(buf, DIM == 256 ? 0 : tile0));
+  };
+  constexpr int kParts = 8 * R::kItems;
   if (v0 < v1) {
-    store_step<DIM>(t, now, sp, win, sinks, tid, lds[0]);
+    const bool key_wave = !(part0 & 1);
+    if (DIM == 256 || !key_wave) hide_values<DIM>(t, R::kItems - 1, tid % DIM, pos_in(now), sp, win, sinks);
+#pragma unroll
+    for (int n = 0; n < kParts; ++n) dequantise(n, 0, key_wave);
     load_step<DIM>(a.kv, head, in, tid, t);
     find_step<DIM>(a, e, sp, v0 + 2 * kTiles, v1, page_shift, ahead);
   }
@@ -234,30 +244,38 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
 
   int buf = 0;
   for (int v = v0; v < v1; v += kTiles, buf ^= 1) {
+    // This step's scores beside the dequantisation of the next step (zeros past
+    // the last one).
+    // (Left to itself the compiler puts one after the other.)
     f16v s[kTiles];
+    auto scores = [&](bool key_wave) {
+      constexpr int kM = kTiles * DIM / 16, kAhead = 4;
+      static_assert(kM == kParts);
+      h8v kf[kM];
+      auto fetch = [&](int n) { kf[n] = keys(buf, n / (DIM / 16))[n % (DIM / 16) * 64 + lane]; };
 #pragma unroll
-    for (int z = 0; z < kTiles; ++z) {
-      const h8v* kt = lds[buf] + (2 * z) * (R::kHalves / 8) + lane;
+      for (int n = 0; n < kAhead; ++n) fetch(n);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) s[z][k] = 0.0f;
+      for (int z = 0; z < kTiles; ++z)
 #pragma unroll
-      for (int k0 = 0; k0 < DIM / 16; k0 += 4) {
-        h8v kf[4];
+        for (int k = 0; k < 16; ++k) s[z][k] = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) kf[ks] = kt[(k0 + ks) * 64];
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) s[z] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[ks], q[k0 + ks], s[z], 0, 0, 0);
+      for (int n = 0; n < kM; ++n) {
+        const int z = n / (DIM / 16);
+        s[z] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[n], q[n % (DIM / 16)], s[z], 0, 0, 0);
+        if (n + kAhead < kM) fetch(n + kAhead);
+        dequantise(n, buf ^ 1, key_wave);
+        if (DIM > 64) __builtin_amdgcn_sched_barrier(0);
       }
-    }
+    };
+    if (DIM == 256 || (part0 & 1)) hide_values<DIM>(t, R::kItems - 1, tid % DIM, pos_in(in), sp, win, sinks);
+    if (DIM == 256 || !(part0 & 1)) scores(true);
+    else scores(false);
     const StepAt<kTiles> cur = now;
-    if (v + kTiles < v1) {
-      store_step<DIM>(t, in, sp, win, sinks, tid, lds[buf ^ 1]);
-      now = in;
-      in = ahead;
-      load_step<DIM>(a.kv, head, in, tid, t);
-      find_step<DIM>(a, e, sp, v + 3 * kTiles, v1, page_shift, ahead);
-    }
+    now = in;
+    in = ahead;
+    load_step<DIM>(a.kv, head, in, tid, t);
+    find_step<DIM>(a, e, sp, v + 3 * kTiles, v1, page_shift, ahead);
     float top = kNegInf;
 #pragma unroll
     for (int z = 0; z < kTiles; ++z) {
