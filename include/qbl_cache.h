@@ -157,10 +157,12 @@ qbl_status qbl_kv_attend_ws_bytes(const qbl_kv* kv, int32_t n, int32_t q_len, in
  * max_len are not read (keys) and queries there are padding.  Rows that see
  * nothing (padding, an empty slot, no page) are 0.  Keys without a page are
  * hidden; what the store holds in hidden places does not matter.
- * Arithmetic: codes enter the matrix cores exactly.  float32: q and the
- * weights as three bf16 parts (24 bits), block steps and minima applied in
- * float32; f16/bf16: see the kernels.  Sums and softmax statistics are
- * float32.  Deterministic. */
+ * Arithmetic: sums and softmax statistics are float32.  float32 and f16 rows: no
+ * key or value is rounded, q (float32) and the weights enter the matrix cores as
+ * two f16 parts (22 bits).  bf16 rows: keys, values and weights are rounded once
+ * to f16 (2^-12 relative).  A row of q that is not finite gives NaN.
+ * Deterministic.  The blocks are taken to be qbl_kv_append's: steps up to 4369
+ * and values up to 32768. */
 qbl_status qbl_kv_attend(const qbl_kv* kv, int32_t layer, const int32_t* slots, const int32_t* counts,
                          int32_t n, int32_t q_len, int32_t n_heads, const void* q, const int64_t q_strides[3],
                          void* out, const int64_t out_strides[3], int32_t dtype, int64_t max_len,

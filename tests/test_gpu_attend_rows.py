@@ -132,3 +132,22 @@ def test_reading_rows_by_tile_pads_with_zeros(q_len):
                 wk[i, j], wv[i, j] = k[i, t], v[i, t]
     for got, want in ((ko, wk), (vo, wv)):
         assert (np.abs(got.double().cpu().numpy() - want) <= 2.0 ** -24 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("q_len", [1, 24, 70])
+@pytest.mark.parametrize("power", [-18, -12, 12])
+def test_values_at_the_ends_of_the_scales_range(power, q_len, dtype):
+    """Steps that are fp16 subnormals, and values near the largest that the cache holds.  (Not with f16 rows:
+    their outputs would be subnormals, whose half step is 2^-25 and not eps/2 of the value.)"""
+    from quantized_base_linear_amd import cache
+    n = 150
+    kv, _, _ = build(64, 32, 1, [n], seed=28)
+    rng = np.random.default_rng(28)
+    k = rng.standard_normal((1, n, 1, 64)).astype(np.float32)
+    v = (rng.standard_normal(k.shape) * 2.0 ** power).astype(np.float32)
+    cache.qbl_kv_append(kv, 0, None, None, torch.tensor(k * 2.0 ** power).float().cuda(), torch.tensor(v).cuda())
+    k, v = ref.values(*ref.quantise(k * np.float32(2.0 ** power))), ref.values(*ref.quantise(v))
+    qt = queries((1, q_len, 2, 64), dtype, 28)
+    out = run(kv, qt, None, n, scale=2.0 ** -power / 8)
+    compare(kv, k, v, qt, [q_len], [n], out, dtype, scale=2.0 ** -power / 8)
