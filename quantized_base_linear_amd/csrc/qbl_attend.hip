@@ -30,7 +30,7 @@
 // (and the sums rescaled) only when a score passes it by 4 in the exponent of
 // 2, so in most tiles no cross-lane step is needed.
 //
-// Vector instructions bound it before memory does: some 230 (bf16) to 450
+// Vector instructions bound it before memory does: some 270 (bf16) to 420
 // (float32) per tile of 5 KB, with 128 channels.  Measured: 32 bf16 requests of
 // 1 to 20000 tokens (64 heads over 8) 106 us, 4.3 TB/s; one float32 row per head
 // over 131071 tokens 45 us, 3.7 TB/s.

@@ -19,7 +19,7 @@ namespace {
 constexpr int kWg = 1024;
 constexpr int kWaves = kWg / 64;
 // Bytes of a page that one workgroup copies at a time: 16 per thread.  64 copies
-// of 320 KB take 9 us so (20 us with 8 or 16 KB); 1070 of them 67 us (5.2 TB/s,
+// of 320 KB take 9 us so (20 us with 8 or 16 KB); 536 of them 70 us (5 TB/s,
 // what a large copy reaches) with any of these.
 constexpr int kPiece = 4096;
 
