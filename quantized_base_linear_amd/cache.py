@@ -103,10 +103,15 @@ class KVCache:
             raise QblError(code, "a page call could not be done; it changed nothing")
 
 
-# The calls below take a few microseconds on the GPU, so their checks are kept short.
+# The calls below take a few microseconds on the GPU, so their checks are one pass over what has to
+# hold; only what fails is looked at again for its message.
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_int32 = torch.int32
+
+
 def _stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -119,6 +124,8 @@ def _ws(ws):
 def _ints(t, numel, what):
     if t is None:
         return None
+    if t.numel() == numel and t.dtype is _int32 and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.numel() != numel:
         raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
     return _dev_ptr(t, torch.int32)
@@ -129,20 +136,21 @@ _Strides = _i64 * 3
 
 def _strided(t, shape, what):
     """Data pointer and strides of an activation tensor whose last dimension is contiguous."""
+    if t.is_cuda and t.shape == shape:
+        *outer, last = t.stride()
+        if last == 1 or shape[-1] == 1:
+            return t.data_ptr(), _Strides(*outer)
+        raise ValueError(f"{what}: the last dimension must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    *outer, last = t.stride()
-    if last != 1 and shape[-1] > 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), _Strides(*outer)
+    raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _dtype(t):
-    if t.dtype not in DTYPES:
+    code = DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"unsupported element type {t.dtype}")
-    return DTYPES[t.dtype]
+    return code
 
 
 def _bytes(nbytes, device):
@@ -207,10 +215,10 @@ def qbl_kv_append(kv: KVCache, layer: int, slots, counts, k, v, stream=None) -> 
 
 def qbl_kv_read(kv: KVCache, layer: int, slots, counts, k_out, v_out, stream=None) -> None:
     """k_out, v_out: float32 [n][q_len][n_kv_heads][head_dim], contiguous."""
-    n, q_len = k_out.shape[0], k_out.shape[1]
-    for t in (k_out, v_out):
-        if tuple(t.shape) != (n, q_len, kv.n_kv_heads, kv.head_dim):
-            raise ValueError(f"outputs must be {(n, q_len, kv.n_kv_heads, kv.head_dim)}")
+    n, q_len = k_out.shape[:2]
+    shape = (n, q_len, kv.n_kv_heads, kv.head_dim)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"outputs must be {shape}")
     _check(_lib.qbl_kv_read(kv.ptr, layer, _ints(slots, n, "slots"), _ints(counts, n, "counts"), n, q_len,
                             _dev_ptr(k_out, torch.float32), _dev_ptr(v_out, torch.float32), _stream(stream)))
 
@@ -260,13 +268,14 @@ def verify_workspace(n: int, vocab: int, device="cuda"):
 def qbl_verify(target, draft, tokens, counts, u, accepted, next_token, ws, stream=None) -> None:
     """target: [n][q_len + 1][vocab] probabilities, draft: [n][q_len][vocab] or None, tokens: int32
     [n][q_len] (None if q_len is 0), u: float32 [n][q_len + 1]; accepted, next_token: int32 [n]."""
-    n, q_len, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
-    tp, ts = _strided(target, (n, q_len + 1, vocab), "target")
+    n, rows, vocab = target.shape
+    q_len = rows - 1
+    tp, ts = _strided(target, (n, rows, vocab), "target")
     dp, ds = (None, None) if draft is None else _strided(draft, (n, q_len, vocab), "draft")
     if draft is not None and draft.dtype != target.dtype:
         raise ValueError("target and draft must have one element type")
-    if u.numel() != n * (q_len + 1):
-        raise ValueError(f"u: expected {n * (q_len + 1)} elements, got {u.numel()}")
+    if u.numel() != n * rows:
+        raise ValueError(f"u: expected {n * rows} elements, got {u.numel()}")
     wp, wb = _ws(ws)
     _check(_lib.qbl_verify(tp, ts, dp, ds, _dtype(target),
                            _ints(tokens, n * q_len, "tokens"), _ints(counts, n, "counts"), _dev_ptr(u, torch.float32), n,
