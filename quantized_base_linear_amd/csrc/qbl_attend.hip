@@ -128,12 +128,8 @@ __device__ __forceinline__ h2v times8(h2v x) { return x * h2v{(_Float16)8.0f, (_
 
 __device__ __forceinline__ f4v mfma(h8v x, h8v y, f4v acc) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, acc, 0, 0, 0); }
 
-// Waves per SIMD that the registers have to leave room for.
 template <int DIM, int T, int NT>
-constexpr int kMinWaves = DIM == 256 || (DIM == 128 && NT == 2 && T == QBL_T_F32) ? 1 : 2;
-
-template <int DIM, int T, int NT>
-__global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kernel(KvAttend a, int row_blocks, int chunk, int splits,
+__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void attend_kernel(KvAttend a, int row_blocks, int chunk, int splits,
                                                           int page_shift, int64_t part_floats) {
   constexpr int kNb = DIM / 32;
   constexpr bool kExact = T != QBL_T_BF16;
@@ -153,12 +149,10 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<DIM, T, NT>)) void attend_kern
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  int b = blockIdx.x;
-  const int split = b % splits;
-  b /= splits;
-  const int rb = b % row_blocks;
-  b /= row_blocks;
-  const int h = b % a.kv.n_kv_heads, i = b / a.kv.n_kv_heads;
+  int pair, part;
+  xcd_pair(blockIdx.x, a.rows.n * a.kv.n_kv_heads, row_blocks * splits, pair, part);
+  const int split = part % splits, rb = part / splits;
+  const int h = pair % a.kv.n_kv_heads, i = pair / a.kv.n_kv_heads;
   const Entry e = load_entry(a.kv, a.rows, i);
   const int r0 = rb * 16 * NT;
   const int win = (int)a.window, sinks = (int)a.sinks;
@@ -647,13 +641,16 @@ hipError_t launch_few(const KvAttend& a, const AttendPlan& p, const LaunchCtx& l
   return hipGetLastError();
 }
 
+constexpr bool two_blocks(int dim, int dtype) { return dim == 64 || (dim == 128 && dtype != QBL_T_F32); }
+
 template <int DIM, int T>
 hipError_t launch_type(const KvAttend& a, const AttendPlan& p, const LaunchCtx& lc) {
   hipError_t e;
   if (p.many) {
     e = launch_attend_rows(a, p, lc);
-  } else if (DIM <= 128 && p.cols == 32) {
-    if constexpr (DIM <= 128) e = launch_few<DIM, T, 2>(a, p, lc);
+  } else if (p.cols == 32) {
+    e = hipErrorInvalidValue;
+    if constexpr (two_blocks(DIM, T)) e = launch_few<DIM, T, 2>(a, p, lc);
   } else {
     e = launch_few<DIM, T, 1>(a, p, lc);
   }
@@ -676,9 +673,10 @@ AttendPlan attend_plan(const KvAttend& a) {
   AttendPlan p;
   const int64_t rows = (int64_t)a.rows.q_len * a.group;
   p.many = a.dtype == QBL_T_BF16 && rows > 32;
-  // Two row blocks per workgroup read the cache once for both; 256 channels
-  // leave registers for one only (two spill).
-  p.cols = p.many ? kManyRows : rows <= 16 || a.kv.head_dim == 256 ? 16 : 32;
+  // Two row blocks per workgroup read the cache once for both.  One where the
+  // registers do not hold two without giving up half of the waves: 256 channels,
+  // and float32 rows of 128 (512 tokens behind 7679: 287 us with one, 345 with two).
+  p.cols = p.many ? kManyRows : rows <= 16 || !two_blocks(a.kv.head_dim, a.dtype) ? 16 : 32;
   p.row_blocks = (int)((rows + p.cols - 1) / p.cols);
   // Tiles that a block of rows can see at most.
   const int64_t len = std::min<int64_t>(a.max_len, (int64_t)a.kv.max_pages * a.kv.page_tokens);
