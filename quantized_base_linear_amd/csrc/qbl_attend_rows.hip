@@ -165,7 +165,14 @@ __global__ __launch_bounds__(kRowThreads, DIM == 256 ? 1 : 2) void attend_rows_k
   const int col = lane & 31, hf = lane >> 5;
   int pair, part;
   xcd_pair(blockIdx.x, a.rows.n * a.kv.n_kv_heads, row_blocks * splits, pair, part);
-  // the rows that see most first: they take longest
+  // Rows that see most take longest and go first.  Where all workgroups are on the
+  // device at once, two per CU, every second 32 of an XCD run the other way, so
+  // that a CU's long one comes with a short one.
+  const int per = row_blocks * splits;
+  if (gridDim.x <= 512 && (int)blockIdx.x < (a.rows.n * a.kv.n_kv_heads & ~7) * per) {
+    const int k = blockIdx.x >> 3, begin = k - part, chunk = k & ~31;  // this XCD's k-th; its pair's first
+    if (k & 32) part = max(chunk, begin) + min(chunk + 32, begin + per) - 1 - k - begin;
+  }
   const int rb = row_blocks - 1 - part / splits, split = part % splits;
   const int h = pair % a.kv.n_kv_heads, i = pair / a.kv.n_kv_heads;
   const Entry e = load_entry(a.kv, a.rows, i);
