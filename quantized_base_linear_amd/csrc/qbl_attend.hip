@@ -672,7 +672,11 @@ hipError_t launch_dim(const KvAttend& a, const AttendPlan& p, const LaunchCtx& l
 AttendPlan attend_plan(const KvAttend& a) {
   AttendPlan p;
   const int64_t rows = (int64_t)a.rows.q_len * a.group;
-  p.many = a.dtype == QBL_T_BF16 && rows > 32;
+  // The many-row kernel is for bf16 only (its keys, values and weights are rounded
+  // once to f16).  It pays from about 64 rows per key/value head on: 8 requests
+  // over 8000 tokens (32 heads over 8, 128 channels) take 45 us here and 55 us
+  // there with 64 rows, 79 and 64 us with 128.
+  p.many = a.dtype == QBL_T_BF16 && rows > 64;
   // Two row blocks per workgroup read the cache once for both.  One where the
   // registers do not hold two without giving up half of the waves: 256 channels,
   // and float32 rows of 128 (512 tokens behind 7679: 287 us with one, 345 with two).
