@@ -151,3 +151,19 @@ def test_values_at_the_ends_of_the_scales_range(power, q_len, dtype):
     qt = queries((1, q_len, 2, 64), dtype, 28)
     out = run(kv, qt, None, n, scale=2.0 ** -power / 8)
     compare(kv, k, v, qt, [q_len], [n], out, dtype, scale=2.0 ** -power / 8)
+
+
+@pytest.mark.parametrize("n,kv_heads,q_len", [(8, 8, 640), (3, 3, 1500), (16, 16, 200)])
+def test_many_workgroups_cover_every_row(n, kv_heads, q_len):
+    """Several (entry, head) pairs per XCD, more workgroups than its CUs, and pairs left over."""
+    lens = [q_len + 7 * i for i in range(n)]
+    kv, k, v = build(64, 64, kv_heads, lens, seed=29)
+    qt = queries((n, q_len, kv_heads, 64), "bf16", 29)
+    out = run(kv, qt, None, max(lens))
+    pick = [0, n - 1]
+    compare(kv, k[pick], v[pick], qt[pick], [q_len] * 2, [lens[i] for i in pick], out[pick], "bf16")
+    alone = [run(kv, qt[i:i + 1].contiguous(), None, max(lens), slots=[i]) for i in range(n)]
+    # an entry by itself is cut along the cache where all together are not: equal up to the outputs' rounding
+    for i in range(n):
+        a, b = out[i].float(), alone[i][0].float()
+        assert float((a - b).norm() / b.norm()) < 2 * 2.0 ** -8
